@@ -29,6 +29,9 @@ __all__ = [
     "msa_prefill_fp8_index", "msa_prefill_varlen_workspace_size", "msa_decode_fp8_index",
     "msa_quantize_rows_fp8", "OP_PREFILL_Q8KV4", "MX_E4M3", "MX_E2M1", "msa_quantize_mx",
     "msa_prefill_q8kv4",
+    "OP_ROPE_APPEND", "OP_DENSE_PREFILL", "OP_DENSE_PREFILL_PAGED", "OP_DENSE_DECODE",
+    "PagedKV", "paged_kv", "msa_rope_append_paged", "msa_dense_prefill_varlen",
+    "msa_dense_prefill_paged", "msa_dense_decode_paged",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -39,6 +42,10 @@ OP_BLOCK_QUERY_LISTS = 1
 OP_PREFILL = 2
 OP_DECODE = 3
 OP_PREFILL_Q8KV4 = 4
+OP_ROPE_APPEND = 5
+OP_DENSE_PREFILL = 6
+OP_DENSE_PREFILL_PAGED = 7
+OP_DENSE_DECODE = 8
 MX_E4M3, MX_E2M1 = 0, 1
 
 STATUS_NAMES = {0: "MSA_OK", 1: "MSA_ERR_INVALID_ARG", 2: "MSA_ERR_UNSUPPORTED",
@@ -58,6 +65,14 @@ class MsaConfig(ctypes.Structure):
         return (f"MsaConfig(H={self.num_heads}, G={self.num_groups}, d={self.head_dim}, "
                 f"d_idx={self.index_dim}, block={self.block_size}, k={self.top_k}, "
                 f"scale={self.softmax_scale:.6g})")
+
+
+class _PagedKVStruct(ctypes.Structure):
+    """Mirror of ``msa_paged_kv_t``."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("table_stride", ctypes.c_int32)]
 
 
 class MsaError(RuntimeError):
@@ -112,6 +127,12 @@ def load_library():
     lib.msa_quantize_rows_fp8.argtypes = [P, I64, P, P, P]
     lib.msa_quantize_mx.argtypes = [P, I64, I32, I32, P, P, P]
     lib.msa_prefill_q8kv4.argtypes = [C, P, P, P, P, P, P, P, P, I64, P, P, P, SZ, P]
+    V = ctypes.POINTER(_PagedKVStruct)
+    lib.msa_rope_append_paged.argtypes = [C, P, I64, P, I64, P, I64, P, I32, I32, V, P, P, I32, I64,
+                                          P, P, SZ, P]
+    lib.msa_dense_prefill_varlen.argtypes = [C, P, P, P, P, I32, P, P, SZ, P]
+    lib.msa_dense_prefill_paged.argtypes = [C, P, V, P, P, I32, I64, P, P, SZ, P]
+    lib.msa_dense_decode_paged.argtypes = [C, P, V, P, I32, P, P, SZ, P]
     lib.msa_get_device_error.argtypes = [P, P, ctypes.POINTER(ctypes.c_uint32)]
     lib.msa_selftest_wait_timeout.argtypes = [P, ctypes.c_uint64, P]
     lib.msa_status_string.argtypes = [ctypes.c_int]
@@ -127,6 +148,8 @@ def load_library():
                  "msa_prefill_varlen", "msa_prefill_varlen_workspace_size",
                  "msa_prefill_block_alignment", "msa_prefill_fp8_index",
                  "msa_quantize_mx", "msa_prefill_q8kv4",
+                 "msa_rope_append_paged", "msa_dense_prefill_varlen", "msa_dense_prefill_paged",
+                 "msa_dense_decode_paged",
                  "msa_decode",
                  "msa_decode_static", "msa_get_device_error", "msa_selftest_wait_timeout"):
         getattr(lib, name).restype = ctypes.c_int
@@ -576,6 +599,253 @@ def msa_decode_static(cfg: MsaConfig, q, q_idx, k_cache, v_cache, k_idx_cache, c
                                ids_ptr, 1 if check_device_error else 0, _stream(stream))
     _check(st, "msa_decode_static")
     return out if ids_out is None else (out, ids_out)
+
+
+class PagedKV:
+    """A paged cache and the block table of one batch (see ``paged_kv``)."""
+
+    __slots__ = ("k", "v", "block_table", "device", "batch", "heads", "dim", "struct", "ref")
+
+    def __init__(self, k, v, block_table):
+        for name, t in (("k_cache", k), ("v_cache", v)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if not t.is_cuda:
+                raise ValueError(f"{name} must live on a CUDA device")
+            if t.dtype != torch.bfloat16:
+                raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+            if t.dim() != 4 or not all(t.shape):
+                raise ValueError(f"{name} must be [pages, page_size, G, d]")
+            if not t[0].is_contiguous():
+                raise ValueError(f"the pages of {name} must be contiguous")
+        if k.shape != v.shape or k.device != v.device:
+            raise ValueError("k_cache and v_cache must have one shape and device")
+        pages, page_size, G, d = k.shape
+        stride = k.stride(0) if pages > 1 else page_size * G * d
+        if pages > 1 and v.stride(0) != stride:
+            raise ValueError("k_cache and v_cache must have the same page stride")
+        if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+            raise ValueError("block_table must be a [B, pages per sequence] tensor")
+        if block_table.device != k.device:
+            raise ValueError("block_table must live on the cache's device")
+        table = _dev(block_table, torch.int32, "block_table")
+        self.k, self.v, self.block_table = k, v, block_table
+        self.device, self.batch, self.heads, self.dim = k.device, block_table.shape[0], G, d
+        self.struct = _PagedKVStruct(k.data_ptr(), v.data_ptr(), table, pages, stride, page_size,
+                                     block_table.shape[1])
+        self.ref = ctypes.byref(self.struct)
+
+
+def paged_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor) -> PagedKV:
+    """The cache argument of the paged calls: k_cache, v_cache [pages, page_size, G, d] bf16 (the
+    page dimension may be strided, e.g. views of one [pages, 2, page_size, G, d] buffer) and
+    block_table [B, pages per sequence] int32.  Keeps the tensors; copies nothing."""
+    return PagedKV(k_cache, v_cache, block_table)
+
+
+def _on(t, device, name: str) -> None:
+    if t.device != device:
+        raise ValueError(f"{name} lives on {t.device}, expected {device}")
+
+
+def _rows(t, name: str, T: int, heads: int, d: int, device) -> Tuple[int, int]:
+    """Pointer and row stride of a [T, heads, d] tensor with contiguous rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != (T, heads, d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, heads, d)}")
+    if t.device != device:
+        raise ValueError(f"{name} lives on {t.device}, expected {device}")
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != d):
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.data_ptr(), st[0] if T > 1 else heads * d
+
+
+class _Call:
+    """Device, stream and scratch of one full-attention call.  Tensors that the binding allocates
+    on a stream other than the current one are kept from reuse until that stream is done."""
+
+    __slots__ = ("device", "stream", "other", "guard")
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError("the tensors must live on a CUDA device")
+        current = torch.cuda.current_stream(device)
+        if stream is None:
+            stream = current
+        elif stream.device != device:
+            raise ValueError(f"stream of {stream.device} for tensors on {device}")
+        self.device = device
+        self.stream = stream
+        self.other = stream.cuda_stream != current.cuda_stream
+        self.guard = None
+
+    def empty(self, shape, dtype):
+        if not self.other:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):  # first use is on that stream
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, ws, cfg, op, T, B):
+        if ws is None:
+            return self.empty((msa_workspace_size(cfg, op, T, B),), torch.uint8)
+        if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != self.device:
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on {self.device}")
+        return ws
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+def _kv_check(cfg: MsaConfig, kv: PagedKV, B: int, device) -> None:
+    if not isinstance(kv, PagedKV):
+        raise TypeError("the cache must be a PagedKV (see paged_kv)")
+    if kv.heads != cfg.num_groups or kv.dim != cfg.head_dim:
+        raise ValueError(f"the cache has {kv.heads} heads of {kv.dim}, expected {cfg.num_groups} "
+                         f"of {cfg.head_dim}")
+    if kv.device != device:
+        raise ValueError(f"the cache lives on {kv.device}, expected {device}")
+    if kv.batch != B:
+        raise ValueError(f"the block table has {kv.batch} rows, expected {B}")
+
+
+def msa_rope_append_paged(cfg: MsaConfig, q, k, v, inv_freq, kv: PagedKV, cu_seqlens, seq_lens,
+                          interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None):
+    """Rotate the new tokens' q [T,H,d] and k [T,G,d] by their positions and append k and v [T,G,d]
+    to the paged cache; the rows of q, k, v may be strided (views of a fused projection).
+
+    ``inv_freq``: float32 [rot/2] on the device; ``cu_seqlens`` int64 [B+1] and ``seq_lens`` int32
+    [B] on the device (see include/msa.h).  Returns the rotated queries [T,H,d] (``q_out``, which
+    may be a contiguous ``q`` itself), or None when ``q`` is None."""
+    lib = load_library()
+    T, dev = k.shape[0], k.device
+    H, G, d = cfg.num_heads, cfg.num_groups, cfg.head_dim
+    B = seq_lens.shape[0]
+    call = _Call(dev, stream)
+    _kv_check(cfg, kv, B, dev)
+    kp, ks = _rows(k, "k", T, G, d, dev)
+    vp, vs = _rows(v, "v", T, G, d, dev)
+    qp, qs, op = None, 0, None
+    if q is not None:
+        qp, qs = _rows(q, "q", T, H, d, dev)
+        if q_out is None:
+            q_out = call.empty((T, H, d), torch.bfloat16)
+        _on(q_out, dev, "q_out")
+        op = _dev(q_out, torch.bfloat16, "q_out", (T, H, d))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    for t, name in ((inv_freq, "inv_freq"), (cu_seqlens, "cu_seqlens"), (seq_lens, "seq_lens")):
+        _on(t, dev, name)
+    ws = call.workspace(workspace, cfg, OP_ROPE_APPEND, T, B)
+    with call:
+        st = lib.msa_rope_append_paged(
+            ctypes.byref(cfg), qp, qs, kp, ks, vp, vs, _dev(inv_freq, torch.float32, "inv_freq"),
+            2 * inv_freq.numel(), 1 if interleaved else 0, kv.ref,
+            _dev(cu_seqlens, torch.int64, "cu_seqlens", (B + 1,)),
+            _dev(seq_lens, torch.int32, "seq_lens", (B,)), B, T, op, ws.data_ptr(), ws.numel(),
+            call.stream.cuda_stream)
+    _check(st, "msa_rope_append_paged")
+    return q_out
+
+
+def msa_dense_prefill_varlen(cfg: MsaConfig, q, k, v, cu_seqlens,
+                             out: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None, stream=None):
+    """Full causal attention of whole prompts packed along the token axis: q [T,H,d], k/v [T,G,d],
+    host ``cu_seqlens`` (any int sequence of B+1 offsets).  Returns out [T,H,d]."""
+    lib = load_library()
+    import numpy as _np
+    cu = _np.ascontiguousarray(_np.asarray(
+        cu_seqlens.cpu() if isinstance(cu_seqlens, torch.Tensor) else cu_seqlens,
+        dtype=_np.int64))
+    B = len(cu) - 1
+    T, dev = q.shape[0], q.device
+    H, G, d = cfg.num_heads, cfg.num_groups, cfg.head_dim
+    if B < 1 or int(cu[-1]) != T:
+        raise ValueError(f"cu_seqlens must end at the packed length {T}")
+    call = _Call(dev, stream)
+    for t, name in ((k, "k"), (v, "v")):
+        _on(t, dev, name)
+    if out is None:
+        out = call.empty((T, H, d), torch.bfloat16)
+    _on(out, dev, "out")
+    ws = call.workspace(workspace, cfg, OP_DENSE_PREFILL, T, B)
+    with call:
+        st = lib.msa_dense_prefill_varlen(
+            ctypes.byref(cfg), _dev(q, torch.bfloat16, "q", (T, H, d)),
+            _dev(k, torch.bfloat16, "k", (T, G, d)), _dev(v, torch.bfloat16, "v", (T, G, d)),
+            cu.ctypes.data, B, _dev(out, torch.bfloat16, "out", (T, H, d)), ws.data_ptr(),
+            ws.numel(), call.stream.cuda_stream)
+    _check(st, "msa_dense_prefill_varlen")
+    return out
+
+
+def msa_dense_prefill_paged(cfg: MsaConfig, q, kv: PagedKV, cu_seqlens, seq_lens,
+                            out: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, stream=None):
+    """Full causal attention of each sequence's new tokens q [T,H,d] over its paged cache, which
+    holds their keys and values already.  ``cu_seqlens`` int64 [B+1] and ``seq_lens`` int32 [B] on
+    the device, as for msa_rope_append_paged.  Returns out [T,H,d]; rows behind the last sequence
+    are left as they were."""
+    lib = load_library()
+    T, dev = q.shape[0], q.device
+    H, d = cfg.num_heads, cfg.head_dim
+    B = seq_lens.shape[0]
+    call = _Call(dev, stream)
+    _kv_check(cfg, kv, B, dev)
+    for t, name in ((cu_seqlens, "cu_seqlens"), (seq_lens, "seq_lens")):
+        _on(t, dev, name)
+    if out is None:
+        out = call.empty((T, H, d), torch.bfloat16)
+    _on(out, dev, "out")
+    ws = call.workspace(workspace, cfg, OP_DENSE_PREFILL_PAGED, T, B)
+    with call:
+        st = lib.msa_dense_prefill_paged(
+            ctypes.byref(cfg), _dev(q, torch.bfloat16, "q", (T, H, d)), kv.ref,
+            _dev(cu_seqlens, torch.int64, "cu_seqlens", (B + 1,)),
+            _dev(seq_lens, torch.int32, "seq_lens", (B,)), B, T,
+            _dev(out, torch.bfloat16, "out", (T, H, d)), ws.data_ptr(), ws.numel(),
+            call.stream.cuda_stream)
+    _check(st, "msa_dense_prefill_paged")
+    return out
+
+
+def msa_dense_decode_paged(cfg: MsaConfig, q, kv: PagedKV, seq_lens,
+                           out: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None):
+    """Full attention of one new token per sequence, q [B,H,d], over its paged cache (its own key
+    and value are in it); ``seq_lens`` int32 [B] on the device.  Returns out [B,H,d], zeros for a
+    sequence of length 0."""
+    lib = load_library()
+    B, dev = q.shape[0], q.device
+    H, d = cfg.num_heads, cfg.head_dim
+    call = _Call(dev, stream)
+    _kv_check(cfg, kv, B, dev)
+    _on(seq_lens, dev, "seq_lens")
+    if out is None:
+        out = call.empty((B, H, d), torch.bfloat16)
+    _on(out, dev, "out")
+    ws = call.workspace(workspace, cfg, OP_DENSE_DECODE, B, B)
+    with call:
+        st = lib.msa_dense_decode_paged(
+            ctypes.byref(cfg), _dev(q, torch.bfloat16, "q", (B, H, d)), kv.ref,
+            _dev(seq_lens, torch.int32, "seq_lens", (B,)), B,
+            _dev(out, torch.bfloat16, "out", (B, H, d)), ws.data_ptr(), ws.numel(),
+            call.stream.cuda_stream)
+    _check(st, "msa_dense_decode_paged")
+    return out
 
 
 _phase_keep = None

@@ -20,7 +20,9 @@ HEADER = os.path.join(ROOT, "include", "msa.h")
 
 SOURCES = ["api.cu", "index_kernel.cu", "csr_kernel.cu", "main_kernel.cu", "merge_kernel.cu",
            "align_kernel.cu", "quant_kernel.cu", "mx_kernel.cu",
-           "decode_kernel.cu", "decode_static.cu", "selftest.cu"]
+           "decode_kernel.cu", "decode_static.cu", "selftest.cu",
+           "api_dense.cu", "rope_append_kernel.cu", "dense_prefill_kernel.cu",
+           "dense_decode_kernel.cu"]
 NVCC = os.environ.get("NVCC", "nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-std=c++17", "-lineinfo",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",

@@ -7,13 +7,13 @@
 #include <string.h>
 
 #include "../../include/msa.h"
+#include "api_common.h"
 #include "kernels.h"
 
 namespace msa {
 namespace {
 
 constexpr int kBlock = 128;
-constexpr size_t kHeader = 256;  // device error word + reserved
 constexpr int kUnitTiles = 16;   // Main Branch tiles per work unit
 
 thread_local int g_launches = 0;
@@ -25,8 +25,6 @@ void mark(int i, cudaStream_t s) {
     cudaEventRecord(static_cast<cudaEvent_t>(g_events[i]), s);
 }
 
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
 msa_status_t check_cfg(const msa_config_t* c) {
@@ -64,14 +62,6 @@ int64_t n_blocks(int64_t n) { return (n + kBlock - 1) / kBlock; }
 size_t mx_dequant_bytes(const msa_config_t* c, int64_t N) {
   return align256((size_t)N * c->num_heads * c->head_dim * 2) +
          2 * align256((size_t)N * c->num_groups * c->head_dim * 2);
-}
-
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return 148;
-  return n;
 }
 
 // ---- prefill workspace: the fp16 copy of V for all N tokens, then the
@@ -156,21 +146,10 @@ DecodeLayout decode_layout(const msa_config_t* c, int32_t B) {
   return l;
 }
 
-template <typename T>
-T* at(void* ws, size_t off) {
-  return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
-}
-
-// A failed launch is reported through the status; the runtime's last-error
-// slot is cleared so that the caller's next, unrelated CUDA call does not
-// see it again (a sticky error stays sticky regardless).
-msa_status_t cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return MSA_OK;
-  (void)cudaGetLastError();
-  return MSA_ERR_CUDA;
-}
-
 }  // namespace
+
+void set_launch_count(int n) { g_launches = n; }
+
 }  // namespace msa
 
 using namespace msa;
@@ -202,6 +181,8 @@ msa_status_t msa_set_phase_events(void* const* events, int32_t count) {
 
 msa_status_t msa_workspace_size(const msa_config_t* cfg, msa_op_t op, int64_t n_tokens,
                                 int32_t batch, size_t* bytes) {
+  if (op >= MSA_OP_ROPE_APPEND && op <= MSA_OP_DENSE_DECODE)
+    return dense_workspace_size(cfg, op, n_tokens, batch, bytes);
   msa_status_t st = check_cfg(cfg);
   if (st != MSA_OK) return st;
   if (!bytes) return MSA_ERR_INVALID_ARG;
@@ -230,7 +211,7 @@ msa_status_t msa_workspace_size(const msa_config_t* cfg, msa_op_t op, int64_t n_
       *bytes = prefill_layout(cfg, n_tokens, n_tokens, nb, true).total +
                mx_dequant_bytes(cfg, n_tokens);
       return MSA_OK;
-    case MSA_OP_DECODE:
+    default:
       break;
   }
   return MSA_ERR_INVALID_ARG;

@@ -191,6 +191,91 @@ cudaError_t launch_mx_quantize(const void* x, int64_t n_blocks, int fmt, void* c
                                uint8_t* scales, int sms, cudaStream_t s);
 cudaError_t launch_mx_dequantize(const void* codes, const uint8_t* scales, int64_t n_blocks,
                                  int fmt, void* out, int sms, cudaStream_t s);
+
+// ---- full attention over packed or paged keys and values --------------------
+// The paged cache of one call (see msa_paged_kv_t); page_size 0: none.
+struct PagedCache {
+  void* k;
+  void* v;  // [num_pages][page_size][G][d] bf16, pages page_stride elements apart
+  const int32_t* block_table;  // [B][table_stride] page ids
+  int64_t num_pages, page_stride;
+  int32_t page_size, table_stride;
+};
+// rotation of new queries and keys, append of keys and values (rope_append_kernel.cu)
+struct RopeAppendLaunch {
+  PagedCache cache;
+  const void* q;  // [T] rows of H*d, q_stride elements apart; null: keys and values only
+  const void* k;
+  const void* v;  // [T] rows of G*d
+  int64_t q_stride, k_stride, v_stride;
+  const float* inv_freq;  // [rot/2]
+  int32_t rot, interleaved;
+  const int64_t* cu;       // [B+1]
+  const int32_t* seq_lens; // [B]
+  int32_t B, H, G, d;
+  int64_t T;
+  void* q_out;  // [T][H][d]
+  uint32_t* err;
+  int num_sms;
+};
+cudaError_t launch_rope_append(const RopeAppendLaunch& p, cudaStream_t s);
+
+// prefill (dense_prefill_kernel.cu).  A unit is up to 2*TT tokens of one sequence
+// against key tiles [kv0, kv1); `slot` >= 0: a part whose result goes to partial
+// slot + g.
+struct alignas(16) DenseUnit {
+  int32_t tok0, ntok, pos0, seq;
+  int32_t kv0, kv1, slot, row0;  // row0: first packed key row of the sequence
+};
+struct alignas(16) DenseSplit {
+  int32_t tok0, ntok, slot, parts;
+};
+constexpr int kDenseMaxSeqs = 1024;  // host offsets passed to one launch
+struct DenseOffsets {
+  int64_t cu[kDenseMaxSeqs + 1];
+};
+struct DensePrefillLaunch {
+  const void* q;  // [T][H][d]
+  const void* k;
+  const void* v;  // packed [T][G][d], or null with a paged cache
+  PagedCache cache;
+  const DenseOffsets* offsets;  // host offsets, used when cu is null
+  const int64_t* cu;            // device [B+1]
+  const int32_t* seq_lens;      // device [B], null with packed keys
+  int32_t B, H, G, d;
+  int64_t T;
+  float scale;
+  void* out;  // [T][H][d]
+  // workspace
+  DenseUnit* units;
+  DenseSplit* splits;
+  int32_t* counts;
+  float* part_o;
+  float2* part_ml;
+  int32_t max_units, max_slots;
+  uint32_t* err;
+  int grid;
+};
+int dense_tile_tokens(int H, int G);  // tokens per 128-row tile
+cudaError_t launch_dense_prefill(const DensePrefillLaunch& p, cudaStream_t s, int* launches);
+
+// one new token per sequence (dense_decode_kernel.cu)
+struct DenseDecodeLaunch {
+  const void* q;  // [B][H][d]
+  PagedCache cache;
+  const int32_t* seq_lens;  // [B]
+  int32_t B, H, G, d;
+  float scale;
+  void* out;         // [B][H][d]
+  int32_t* tickets;  // [B][head chunks], zero at launch
+  float* part;       // [grid][2][dense_decode_partial_floats()]
+  uint32_t* err;
+  int grid;
+};
+int dense_decode_chunks(int H, int G);  // (group, heads) items per sequence
+size_t dense_decode_partial_floats(int H, int G, int d);
+cudaError_t launch_dense_decode(const DenseDecodeLaunch& p, cudaStream_t s);
+
 // floats of one split partial of the decode attention: [heads][d] + max + sum
 size_t decode_partial_floats(int32_t H, int32_t G, int32_t d);
 constexpr int kDecodeMaxSplit = 4;

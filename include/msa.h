@@ -32,7 +32,7 @@
  *    returns MSA_ERR_CUDA.  Kernels never trap: a wait that runs out, a bad
  *    index or an input value out of range is recorded in a device error word
  *    inside the workspace and read back with msa_get_device_error.
- *  - Supported shapes: block_size 128; head_dim and index_dim 64 or 128;
+ *  - Supported shapes (the full-attention calls state their own): block_size 128; head_dim and index_dim 64 or 128;
  *    1 <= top_k <= 32; G divides 128; H/G is a power of two with
  *    (H/G) * head_dim <= 2048; 1 <= N < 2^26.  Others return
  *    MSA_ERR_UNSUPPORTED.
@@ -87,7 +87,11 @@ typedef enum {
   MSA_OP_BLOCK_QUERY_LISTS = 1,
   MSA_OP_PREFILL = 2,
   MSA_OP_DECODE = 3,
-  MSA_OP_PREFILL_Q8KV4 = 4
+  MSA_OP_PREFILL_Q8KV4 = 4,
+  MSA_OP_ROPE_APPEND = 5,
+  MSA_OP_DENSE_PREFILL = 6,
+  MSA_OP_DENSE_PREFILL_PAGED = 7,
+  MSA_OP_DENSE_DECODE = 8
 } msa_op_t;
 
 /*
@@ -99,6 +103,8 @@ typedef enum {
  *   DECODE: n_tokens = total cache rows (sum of sequence lengths), batch = B.
  *   PREFILL_Q8KV4: n_tokens = N; the PREFILL size plus the dequantised
  *     q, k, v (bf16) that msa_prefill_q8kv4 keeps at the end of its workspace.
+ *   ROPE_APPEND, DENSE_PREFILL, DENSE_PREFILL_PAGED: n_tokens = T new tokens,
+ *     batch = B sequences.  DENSE_DECODE: n_tokens = batch = B.
  * Host-only; returns MSA_ERR_INVALID_ARG / MSA_ERR_UNSUPPORTED like the op.
  */
 MSA_API msa_status_t msa_workspace_size(const msa_config_t* cfg, msa_op_t op, int64_t n_tokens,
@@ -408,6 +414,114 @@ MSA_API msa_status_t msa_decode_static(const msa_config_t* cfg, const void* q, c
                                        int32_t B, int64_t max_seqlen, int64_t total_len,
                                        void* out, int32_t* ids_out, int32_t check_device_error,
                                        msa_stream_t stream);
+
+/*
+ * Full (dense) causal attention next to the block-sparse one: the layers of a
+ * model that attend to every key, contexts short enough that top_k blocks hold
+ * them all, and the baseline that MSA's speed-ups are quoted against (zhaixingw
+ * M3 review, section "这套注意力到底怎么省的").  The pages describe no kernel for
+ * it.  Of the configuration these four calls read num_heads, num_groups,
+ * head_dim and softmax_scale; any num_groups that divides num_heads (<= 4096)
+ * with H/G <= 128 is supported, and head_dim 64 or 128.
+ *
+ * A paged cache holds the keys and values of many sequences in pages of
+ * page_size tokens; sequence b's token p is row p % page_size of page
+ * block_table[b][p / page_size].
+ *   k, v        [num_pages][page_size][G][d] bf16, device; consecutive pages are
+ *               page_stride elements apart (a multiple of 8, at least
+ *               page_size*G*d; more when k and v of a page lie side by side)
+ *   block_table [B][table_stride] int32, device.  Entries past a sequence's
+ *               last page are not read.  An entry outside [0, num_pages) is
+ *               recorded as MSA_ERR_DEVICE_INDEX: the append skips the token's
+ *               keys and values, the attention reads zeros in its place.
+ *   page_size   16, 32, 64, 128 or 256; table_stride * page_size <= 2^30.
+ * Memory past a sequence's last token may hold anything, NaN included.
+ * The same cu_seqlens (device, int64 [B+1], ascending) and seq_lens (device,
+ * int32 [B]) describe a step to the append and to the attention: sequence b's
+ * new tokens are rows cu_seqlens[b] .. cu_seqlens[b+1]-1, and seq_lens[b] is its
+ * length with them, so row i is position seq_lens[b] - (cu_seqlens[b+1] - i).
+ * Rows of the T given that lie behind cu_seqlens[B] are left as they are.  A
+ * sequence whose seq_lens is smaller than its new tokens or beyond its row of
+ * the block table is recorded as MSA_ERR_DEVICE_INDEX and skipped.
+ * Sequences must not share a page that one of them appends to.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  const int32_t* block_table;
+  int64_t num_pages;
+  int64_t page_stride;
+  int32_t page_size;
+  int32_t table_stride;
+} msa_paged_kv_t;
+
+/*
+ * Rotary position embedding of new queries and keys, and the append of keys and
+ * values to a paged cache, in one pass.
+ *   q [T] rows of H*d, k and v [T] rows of G*d bf16, device, rows q_stride,
+ *     k_stride, v_stride elements apart (multiples of 8; the three may be views
+ *     of one fused projection's rows).  q and q_out may both be NULL.
+ *   inv_freq [rot_dim/2] fp32, device: token p's dimension pair j is turned by
+ *     the angle p * inv_freq[j] (formed and reduced in fp64).  rot_dim is a
+ *     multiple of 16, at most d; dimensions from rot_dim on are copied (0: all
+ *     of them, and inv_freq may be NULL).
+ *   interleaved: 0 pairs dimension j with j + rot_dim/2, otherwise 2j with 2j+1.
+ *   q_out [T][H][d] bf16 out; may be q itself when q_stride is H*d.
+ *   cache: k (rotated) and v rows are written; nothing else of it is.
+ *   ws: at least msa_workspace_size(cfg, MSA_OP_ROPE_APPEND, T, B).
+ */
+MSA_API msa_status_t msa_rope_append_paged(const msa_config_t* cfg, const void* q,
+                                           int64_t q_stride, const void* k, int64_t k_stride,
+                                           const void* v, int64_t v_stride, const float* inv_freq,
+                                           int32_t rot_dim, int32_t interleaved,
+                                           const msa_paged_kv_t* cache, const int64_t* cu_seqlens,
+                                           const int32_t* seq_lens, int32_t B, int64_t T,
+                                           void* q_out, void* ws, size_t ws_bytes,
+                                           msa_stream_t stream);
+
+/*
+ * Full causal attention of B whole prompts packed along the token axis (no
+ * attention across sequences): the counterpart of msa_prefill_varlen.
+ *   q [T][H][d], k/v [T][G][d] bf16, T = cu_seqlens[B].
+ *   cu_seqlens [B+1] int64, HOST pointer: cu_seqlens[0] = 0, non-decreasing, at
+ *     least one non-empty sequence.
+ *   out [T][H][d] bf16 out: softmax over the keys s <= t of the token's sequence
+ *     of softmax_scale*<q[t][h], k[s][g]>, times v[s][g]; fp32 scores, sums and
+ *     accumulation, probabilities rounded to bf16 for the product with v.  An
+ *     infinity or NaN in a key or value reaches only the tokens that see it.
+ *   ws: at least msa_workspace_size(cfg, MSA_OP_DENSE_PREFILL, T, B).
+ */
+MSA_API msa_status_t msa_dense_prefill_varlen(const msa_config_t* cfg, const void* q,
+                                              const void* k, const void* v,
+                                              const int64_t* cu_seqlens, int32_t B, void* out,
+                                              void* ws, size_t ws_bytes, msa_stream_t stream);
+
+/*
+ * Full causal attention of each sequence's new tokens over its paged cache,
+ * which holds their keys and values already (msa_rope_append_paged): the next
+ * chunk of a long prompt, a prompt behind a cached prefix, a whole prompt, or a
+ * few drafted tokens.  Long caches are split over the GPU when the rows alone
+ * would not fill it.
+ *   q [T][H][d] bf16; out [T][H][d] bf16 out, as in msa_dense_prefill_varlen.
+ *   ws: at least msa_workspace_size(cfg, MSA_OP_DENSE_PREFILL_PAGED, T, B).
+ */
+MSA_API msa_status_t msa_dense_prefill_paged(const msa_config_t* cfg, const void* q,
+                                             const msa_paged_kv_t* cache,
+                                             const int64_t* cu_seqlens, const int32_t* seq_lens,
+                                             int32_t B, int64_t T, void* out, void* ws,
+                                             size_t ws_bytes, msa_stream_t stream);
+
+/*
+ * Full attention of one new token per sequence over its paged cache (its own
+ * key and value are in it): the counterpart of msa_decode.
+ *   q [B][H][d] bf16; seq_lens [B] int32, device, >= 0.
+ *   out [B][H][d] bf16 out; a sequence of length 0 gets zeros.
+ *   ws: at least msa_workspace_size(cfg, MSA_OP_DENSE_DECODE, B, B).
+ */
+MSA_API msa_status_t msa_dense_decode_paged(const msa_config_t* cfg, const void* q,
+                                            const msa_paged_kv_t* cache, const int32_t* seq_lens,
+                                            int32_t B, void* out, void* ws, size_t ws_bytes,
+                                            msa_stream_t stream);
 
 /*
  * Reads and clears the device error word of a workspace used by the calls
