@@ -45,8 +45,8 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kCleanWarp0 = 10;
 constexpr int kCleanThreads = 64;
-constexpr uint32_t kRegSoftmax = 224, kRegOther = 56;
-constexpr int kLaunchRegs = 168;  // 2*128*224 + 128*56 = 384*168
+constexpr uint32_t kRegSoftmax = 208, kRegOther = 88;
+constexpr int kLaunchRegs = 168;  // 2*128*208 + 128*88 = 384*168
 constexpr int kRows = 128, kKeys = 128;
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -57,11 +57,24 @@ template <int D>
 struct PrefillCfg {
   static constexpr int kChunks = D / 64;           // 128-byte column chunks
   static constexpr int kTileBytes = kRows * D * 2;  // Q, K and V tiles alike
-  static constexpr int kOffK = 2 * kTileBytes;
-  static constexpr int kOffV = kOffK + 2 * kTileBytes;
-  static constexpr int kOffStage = kOffV + 2 * kTileBytes;
-  static constexpr int kStageWarp = 32 * 128;  // one warp's rows x 64 columns, bf16
-  static constexpr int kSmem = kOffStage + 8 * kStageWarp + 1024;
+  // one ring for K and V tiles in the order of their use (K0 V0 K1 V1 ...): what
+  // 224 KiB hold beside the two Q tiles.  A tile takes some 2000 cycles to come
+  // from L2; with two K and two V tiles the MMAs waited for it.
+  static constexpr int kSlots = D == 128 ? 5 : 10;
+  // P handed over in two parts (96 and 32 keys): 680 against 644 TFLOP/s at d = 64
+  // (8K prompt, 64 heads), nothing gained at d = 128 (1161 against 1176)
+  static constexpr bool kSplitP = D == 64;
+  static constexpr int kOffRing = 2 * kTileBytes;
+  static constexpr int kSmem = kOffRing + kSlots * kTileBytes + 1024;
+};
+
+// position in the ring: slot and the parity of its use
+template <int N>
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) slot = 0, phase ^= 1;
+  }
 };
 
 struct PrefillArgs {
@@ -132,12 +145,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;
-  uint8_t* sK = smem + Cfg::kOffK;
-  uint8_t* sV = smem + Cfg::kOffV;
+  uint8_t* sR = smem + Cfg::kOffRing;
   __shared__ uint64_t bar_q_full[2], bar_q_empty[2];
-  __shared__ uint64_t bar_k_full[2], bar_k_empty[2];
-  __shared__ uint64_t bar_v_full[2], bar_v_empty[2], bar_v_clean[2];
-  __shared__ uint64_t bar_s_full[2], bar_p_full[2], bar_pv_done[2];
+  __shared__ uint64_t bar_full[Cfg::kSlots], bar_empty[Cfg::kSlots];
+  __shared__ uint64_t bar_clean[2];  // V tiles cleaned, in turn
+  __shared__ uint64_t bar_s_full[2], bar_p_most[2], bar_p_full[2], bar_pv_done[2], bar_drain;
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
   __shared__ int odd_v[kFlagSlots];  // an infinity or NaN was taken out of the unit's V
@@ -148,15 +160,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_q_full[i], 1);
       mbar_init(&bar_q_empty[i], 1);
-      mbar_init(&bar_k_full[i], 1);
-      mbar_init(&bar_k_empty[i], 1);
-      mbar_init(&bar_v_full[i], 1);
-      mbar_init(&bar_v_empty[i], 1);
-      mbar_init(&bar_v_clean[i], kCleanThreads);
+      mbar_init(&bar_clean[i], kCleanThreads);
       mbar_init(&bar_s_full[i], 1);
+      mbar_init(&bar_p_most[i], 128);
       mbar_init(&bar_p_full[i], 128);
       mbar_init(&bar_pv_done[i], 1);
     }
+    for (int i = 0; i < Cfg::kSlots; ++i) {
+      mbar_init(&bar_full[i], 1);
+      mbar_init(&bar_empty[i], 1);
+    }
+    mbar_init(&bar_drain, 1);
     for (int i = 0; i < kFlagSlots; ++i) odd_v[i] = 0;
     fence_mbar_init();
   }
@@ -181,8 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&map_k);
         tma_prefetch_desc(&map_v);
       }
-      int t = 0;                  // key tiles loaded so far
-      int kl = 0, vl = 0;         // copies of K and of V issued
+      Ring<Cfg::kSlots> ring;
+      uint32_t loads = 0;         // copies into the ring so far
       uint32_t qn[2] = {0, 0};    // Q tiles loaded so far
       bool ok = true;
       const int boxes = a.page_size == 0 ? 1 : (a.page_size >= kKeys ? 1 : kKeys / a.page_size);
@@ -202,22 +216,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (ok) ++qn[i];
       };
-      // tile j of the unit's keys (or values) into `dst`: one box per page, a
-      // lane each; pages past the sequence's end are not read
-      auto load_kv = [&](const CUtensorMap* map, uint64_t* full, uint64_t* empty, uint8_t* dst,
-                         const Unit& u, int j, int32_t row, int32_t page, int nbox) {
+      // the next tile into the ring: one box per page, a lane each; pages past
+      // the sequence's end are not read
+      auto load_kv = [&](const CUtensorMap* map, int g, int32_t row, int32_t page, int nbox) {
+        if (!ok) return;
+        uint64_t* full = &bar_full[ring.slot];
         if (lane == 0) {
-          ok = mbar_wait(empty, ((t >> 1) & 1) ^ 1, abort_flag, a.err, kDevTimeoutMma);
+          ok = mbar_wait(&bar_empty[ring.slot], ring.phase ^ 1, abort_flag, a.err, kDevTimeoutMma);
           if (ok) mbar_arrive_expect_tx(full, (uint32_t)(nbox * box_rows * D * 2));
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (ok && lane < nbox) {
+        if (!ok) return;
+        if (lane < nbox) {
+          uint8_t* dst = sR + ring.slot * Cfg::kTileBytes + lane * box_rows * 128;
 #pragma unroll
           for (int c = 0; c < Cfg::kChunks; ++c)
-            tma_load_5d(dst + c * kKeys * 128 + lane * box_rows * 128, map, full, 0, row, c, u.g,
-                        page);
+            tma_load_5d(dst + c * kKeys * 128, map, full, 0, row, c, g, page);
         }
         __syncwarp();
+        ++loads;
+        ring.next();
       };
       for (int r = 0; r < rounds && ok; ++r) {
         Unit u;
@@ -243,19 +261,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (j == 0) load_q(u, 0);
-          if (!ok) break;
-          const int st = t & 1;
-          load_kv(&map_k, &bar_k_full[st], &bar_k_empty[st], sK + st * Cfg::kTileBytes, u, j, row,
-                  page, nbox);
-          if (!ok) break;
-          ++kl;
+          load_kv(&map_k, u.g, row, page, nbox);
           if (j == 0) load_q(u, 1);
-          if (!ok) break;
-          load_kv(&map_v, &bar_v_full[st], &bar_v_empty[st], sV + st * Cfg::kTileBytes, u, j, row,
-                  page, nbox);
-          if (!ok) break;
-          ++vl;
-          ++t;
+          load_kv(&map_v, u.g, row, page, nbox);
         }
       }
       if (lane == 0 && *abort_flag) {
@@ -263,104 +271,125 @@ __global__ void __launch_bounds__(kThreads, 1)
         volatile int no_abort = 0;
         for (int i = 0; i < 2; ++i)
           if (qn[i]) mbar_wait(&bar_q_full[i], (qn[i] - 1) & 1, &no_abort, nullptr, 0);
-        for (int x = kl > 2 ? kl - 2 : 0; x < kl; ++x)
-          mbar_wait(&bar_k_full[x & 1], (x >> 1) & 1, &no_abort, nullptr, 0);
-        for (int x = vl > 2 ? vl - 2 : 0; x < vl; ++x)
-          mbar_wait(&bar_v_full[x & 1], (x >> 1) & 1, &no_abort, nullptr, 0);
+        for (uint32_t x = loads > Cfg::kSlots ? loads - Cfg::kSlots : 0; x < loads; ++x)
+          mbar_wait(&bar_full[x % Cfg::kSlots], (x / Cfg::kSlots) & 1, &no_abort, nullptr, 0);
       }
     } else if (warp == kMmaWarp) {
-      // ---------------- MMA issuer (one thread) ----------------
-      if (lane == 0) {
-        constexpr uint32_t idesc_s = idesc_bf16(kRows, kKeys, false, false);
-        constexpr uint32_t idesc_o = idesc_bf16(kRows, D, false, true);
-        const uint32_t q_base = smem_u32(sQ), k_base = smem_u32(sK), v_base = smem_u32(sV);
-        uint32_t qn[2] = {0, 0}, pn[2] = {0, 0}, cn[2] = {0, 0};
-        int t = 0;
-        bool ok = true;
-        uint64_t* last_bar = nullptr;
-        uint32_t last_par = 0, pvn[2] = {0, 0}, scn[2] = {0, 0};
-        auto issue_s = [&](int i, int st) {
+      // ---------------- MMA issuer ----------------
+      // The whole warp walks the units, so that the operands of the MMAs are
+      // warp-uniform (uniform registers); one lane issues.  With the walk in
+      // one lane alone a batch of eight MMAs took 870 cycles to issue.
+      constexpr uint32_t idesc_s = idesc_bf16(kRows, kKeys, false, false);
+      constexpr uint32_t idesc_o = idesc_bf16(kRows, D, false, true);
+      constexpr uint32_t kTile16 = Cfg::kTileBytes / 16;  // descriptor units
+      const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t k_desc = smem_desc_sw128(smem_u32(sR), 16, 1024);
+      const uint64_t v_desc = smem_desc_sw128(smem_u32(sR), kKeys * 128, 1024);
+      uint32_t qn[2] = {0, 0}, pn[2] = {0, 0}, cleaned = 0;
+      Ring<Cfg::kSlots> ring;
+      bool ok = true;
+      auto issue_s = [&](int i, uint32_t slot, bool last) {
+        if (elect_one()) {
+          const uint64_t qd = q_desc + (uint32_t)i * kTile16, kd = k_desc + slot * kTile16;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * kRows * 128 + (kk & 3) * 32;
-            umma_bf16(tmem + kColS + i * 128,
-                      smem_desc_sw128(q_base + i * Cfg::kTileBytes + off, 16, 1024),
-                      smem_desc_sw128(k_base + st * Cfg::kTileBytes + off, 16, 1024), idesc_s,
-                      kk > 0 ? 1u : 0u);
+            const uint32_t off = ((kk >> 2) * kRows * 128 + (kk & 3) * 32) / 16;
+            umma_bf16(tmem + kColS + i * 128, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
           }
           umma_commit(&bar_s_full[i]);
-          last_bar = &bar_s_full[i];
-          last_par = scn[i]++ & 1;
-        };
-        for (int r = 0; r < rounds && ok; ++r) {
-          Unit u;
-          if (!get_unit(a, total, r, u)) continue;
-          const int cnt[2] = {u.c0, u.c1};
-          const int part0 = first_partial(u) - u.d.kv0;
-          ok = mbar_wait(&bar_k_full[t & 1], (t >> 1) & 1, abort_flag, a.err, kDevTimeoutLoad);
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (cnt[i] == 0) continue;
-            ok = mbar_wait(&bar_q_full[i], qn[i] & 1, abort_flag, a.err, kDevTimeoutLoad);
-            if (!ok) break;
-            ++qn[i];
+          if (last) umma_commit(&bar_q_empty[i]);
+        }
+        __syncwarp();
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err, code));
+        return ok;
+      };
+      for (int r = 0; r < rounds && ok; ++r) {
+        Unit u;
+        if (!get_unit(a, total, r, u)) continue;
+        // broadcasts: known to be the same in every lane
+        const int nt = __shfl_sync(0xffffffffu, u.nt, 0);
+        const int cnt[2] = {__shfl_sync(0xffffffffu, u.c0, 0), __shfl_sync(0xffffffffu, u.c1, 0)};
+        const int part0 = __shfl_sync(0xffffffffu, first_partial(u) - u.d.kv0, 0);
+        if (!wait(&bar_full[ring.slot], ring.phase, kDevTimeoutLoad)) break;
+        uint32_t k_slot = ring.slot;
+        ring.next();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (cnt[i] == 0) continue;
+          if (!wait(&bar_q_full[i], qn[i] & 1, kDevTimeoutLoad)) break;
+          ++qn[i];
+          tc_fence_after();
+          issue_s(i, k_slot, cnt[i] == 1);
+        }
+        if (!ok) break;
+        if (elect_one()) umma_commit(&bar_empty[k_slot]);
+        __syncwarp();
+        for (int j = 0; j < nt; ++j) {
+          const uint32_t v_slot = ring.slot;
+          // V as loaded, or cleaned where some row does not see the whole tile
+          if (j >= part0) {
+            if (!wait(&bar_clean[cleaned & 1], (cleaned >> 1) & 1, kDevTimeoutConsumer)) break;
+            ++cleaned;
+          } else {
+            if (!wait(&bar_full[v_slot], ring.phase, kDevTimeoutLoad)) break;
+          }
+          ring.next();
+          if (j + 1 < nt) {
+            if (!wait(&bar_full[ring.slot], ring.phase, kDevTimeoutLoad)) break;
+            k_slot = ring.slot;
+            ring.next();
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (j >= cnt[i]) continue;
+            const uint64_t vd = v_desc + v_slot * kTile16;
+            auto issue_pv = [&](int kk) {  // keys 16kk .. 16kk+15
+              umma_f16_ts(tmem + kColO + i * 128, tmem + kColS + i * 128 + kk * 8,
+                          vd + (uint32_t)(kk * 16 * 128 / 16), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+            };
+            if (Cfg::kSplitP) {
+              if (!wait(&bar_p_most[i], pn[i] & 1, kDevTimeoutConsumer)) break;
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 6; ++kk) issue_pv(kk);
+              }
+              __syncwarp();
+            }
+            if (!wait(&bar_p_full[i], pn[i] & 1, kDevTimeoutConsumer)) break;
+            ++pn[i];
             tc_fence_after();
-            issue_s(i, t & 1);
-            if (cnt[i] == 1) umma_commit(&bar_q_empty[i]);
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = Cfg::kSplitP ? 6 : 0; kk < 8; ++kk) issue_pv(kk);
+              umma_commit(&bar_pv_done[i]);
+            }
+            __syncwarp();
+            if (j + 1 < cnt[i]) issue_s(i, k_slot, j + 2 == cnt[i]);
           }
           if (!ok) break;
-          umma_commit(&bar_k_empty[t & 1]);
-          for (int j = 0; j < u.nt && ok; ++j, ++t) {
-            const int st = t & 1, sn = st ^ 1;
-            // V as loaded, or cleaned where some row does not see the whole tile
-            if (j >= part0) {
-              ok = mbar_wait(&bar_v_clean[st], cn[st] & 1, abort_flag, a.err, kDevTimeoutConsumer);
-              ++cn[st];
-            } else {
-              ok = mbar_wait(&bar_v_full[st], (t >> 1) & 1, abort_flag, a.err, kDevTimeoutLoad);
-            }
-            bool have_k = false;
-            for (int i = 0; i < 2 && ok; ++i) {
-              if (j >= cnt[i]) continue;
-              ok = mbar_wait(&bar_p_full[i], pn[i] & 1, abort_flag, a.err, kDevTimeoutConsumer);
-              if (!ok) break;
-              ++pn[i];
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < kKeys / 16; ++kk)
-                umma_f16_ts(tmem + kColO + i * 128, tmem + kColS + i * 128 + kk * 8,
-                            smem_desc_sw128(v_base + st * Cfg::kTileBytes + kk * 16 * 128,
-                                            kKeys * 128, 1024),
-                            idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-              umma_commit(&bar_pv_done[i]);
-              last_bar = &bar_pv_done[i];
-              last_par = pvn[i]++ & 1;
-              if (j + 1 < cnt[i]) {
-                if (!have_k) {
-                  ok = mbar_wait(&bar_k_full[sn], ((t + 1) >> 1) & 1, abort_flag, a.err,
-                                 kDevTimeoutLoad);
-                  if (!ok) break;
-                  have_k = true;
-                  tc_fence_after();
-                }
-                issue_s(i, sn);
-                if (j + 2 == cnt[i]) umma_commit(&bar_q_empty[i]);
-              }
-            }
-            if (!ok) break;
-            umma_commit(&bar_v_empty[st]);
-            if (j + 1 < u.nt) umma_commit(&bar_k_empty[sn]);
+          if (elect_one()) {
+            umma_commit(&bar_empty[v_slot]);
+            if (j + 1 < nt) umma_commit(&bar_empty[k_slot]);
           }
+          __syncwarp();
         }
-        if (*abort_flag) {
-          // every product issued must be done before TMEM and shared memory go
-          volatile int no_abort = 0;
-          if (last_bar) mbar_wait(last_bar, last_par, &no_abort, nullptr, 0);
-        }
+      }
+      // after an abort every product issued must be done before TMEM and shared
+      // memory go; the drain barrier is used for nothing else
+      if (*abort_flag && elect_one()) {
+        volatile int no_abort = 0;
+        umma_commit(&bar_drain);
+        mbar_wait(&bar_drain, 0, &no_abort, nullptr, 0);
       }
     } else {
       // ---------------- cleaning of V ----------------
       const int x = (int)threadIdx.x - kCleanWarp0 * 32;
-      int t = 0, n = 0;
+      Ring<Cfg::kSlots> ring;
+      int n = 0;
+      uint32_t cleaned = 0;
       bool ok = true;
       for (int r = 0; r < rounds && ok; ++r) {
         Unit u;
@@ -368,12 +397,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int part0 = first_partial(u) - u.d.kv0;
         const int keys_end = u.d.pos0 + u.d.ntok;
         if (x == 0) odd_v[n % kFlagSlots] = 0;
-        for (int j = 0; j < u.nt && ok; ++j, ++t) {
-          const int st = t & 1;
-          ok = mbar_wait(&bar_v_full[st], (t >> 1) & 1, abort_flag, a.err, kDevTimeoutLoad);
+        for (int j = 0; j < u.nt && ok; ++j) {
+          ring.next();  // past the K tile
+          const uint32_t slot = ring.slot;
+          ok = mbar_wait(&bar_full[slot], ring.phase, abort_flag, a.err, kDevTimeoutLoad);
+          ring.next();
           if (!ok || j < part0) continue;
           const int key0 = (u.d.kv0 + j) * kKeys;
-          uint8_t* base = sV + st * Cfg::kTileBytes;
+          uint8_t* base = sR + slot * Cfg::kTileBytes;
           bool odd = false;
           // 16-byte pieces, 8 per 128-byte line, lines chunk-major; where a
           // piece lies within its line does not matter
@@ -404,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (odd) odd_v[n % kFlagSlots] = 1;
           fence_async_smem();
-          mbar_arrive(&bar_v_clean[st]);
+          mbar_arrive(&bar_clean[cleaned++ & 1]);
         }
         ++n;
       }
@@ -420,7 +451,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = lane_addr + kColS + i * 128;
     const uint32_t o_addr = lane_addr + kColO + i * 128;
     const uint64_t k2 = f2_pack(a.scale_log2, a.scale_log2);
-    uint8_t* stage = smem + Cfg::kOffStage + warp * Cfg::kStageWarp;
     uint32_t sn = 0, pvn = 0;
     int n = 0;
     bool ok = true;
@@ -495,10 +525,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x2 = 0; x2 < 16; ++x2) {
             const int col = 32 * q4 + 2 * x2;
-            float a0, a1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[col]), __uint_as_float(s[col + 1])), k2, nm2),
-                      a0, a1);
-            const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+            const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[col]), __uint_as_float(s[col + 1])),
+                                      k2, nm2);
+            float p0, p1;
+            f2_unpack(x, p0, p1);
+            p0 = fast_exp2(p0), p1 = fast_exp2(p1);
             w[x2] = pack_bf16x2(p0, p1);
             if (x2 & 1)
               acc_b = f2_add(acc_b, f2_pack(p0, p1));
@@ -506,6 +537,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               acc_a = f2_add(acc_a, f2_pack(p0, p1));
           }
           tmem_st_32x32b_x16(s_addr + 16 * q4, w);
+          if (Cfg::kSplitP && q4 == 2) {  // the product with the first 96 keys' values may start
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bar_p_most[i]);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -563,55 +599,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const float inv = 1.f / l;
+      __nv_bfloat16* dst =
+          a.out + (((int64_t)u.d.tok0 + tok) * a.H + u.g * a.HG + (row - tt * a.HG)) * D;
 #pragma unroll 1
-      for (int h = 0; h < Cfg::kChunks; ++h) {
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(o_addr + c, o);
+        tmem_wait();
+        reg_fence(o);
+        if (!valid) continue;
+        float f[32];
 #pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-          uint32_t o[16];
-          tmem_ld_32x32b_x16(o_addr + h * 64 + c4 * 16, o);
-          tmem_wait();
-          reg_fence(o);
-          float f[16];
+        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * inv;
+        if (odd) {
+          for (int s = u.d.pos0 + 1; s <= pos; ++s) {
+            const __nv_bfloat16* vr = v_row(a, u, s, D);
+            if (!vr) continue;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(o[e]) * inv;
-          if (odd && valid) {
-            for (int s = u.d.pos0 + 1; s <= pos; ++s) {
-              const __nv_bfloat16* vr = v_row(a, u, s, D);
-              if (!vr) continue;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float v = __bfloat162float(vr[h * 64 + c4 * 16 + e]);
-                if (!(fabsf(v) <= 3.4e38f)) f[e] += v;
-              }
+            for (int e = 0; e < 32; ++e) {
+              const float v = __bfloat162float(vr[c + e]);
+              if (!(fabsf(v) <= 3.4e38f)) f[e] += v;
             }
           }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint4 w;
-            w.x = pack_bf16x2(f[8 * e], f[8 * e + 1]);
-            w.y = pack_bf16x2(f[8 * e + 2], f[8 * e + 3]);
-            w.z = pack_bf16x2(f[8 * e + 4], f[8 * e + 5]);
-            w.w = pack_bf16x2(f[8 * e + 6], f[8 * e + 7]);
-            *reinterpret_cast<uint4*>(stage + sw128_offset(lane, c4 * 2 + e)) = w;
-          }
         }
-        __syncwarp();
-        // 4 rows of 128 bytes per instruction
+        uint32_t w[16];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int rr = k * 4 + (lane >> 3);
-          const int rrow = quarter * 32 + rr;
-          const int rtt = rrow / a.HG;
-          const int rtok = i * a.TT + rtt;
-          if (rtt < a.TT && rtok < u.d.ntok) {
-            const uint4 w = *reinterpret_cast<const uint4*>(stage + sw128_offset(rr, lane & 7));
-            __nv_bfloat16* o = a.out +
-                               (((int64_t)u.d.tok0 + rtok) * a.H + u.g * a.HG + (rrow - rtt * a.HG)) * D +
-                               h * 64;
-            reinterpret_cast<uint4*>(o)[lane & 7] = w;
-          }
-        }
-        __syncwarp();
+        for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+        // a row's 32-byte sectors whole: no staging for coalesced stores
+        st_global_32(dst + c, w);
+        st_global_32(dst + c + 16, w + 8);
       }
       tc_fence_before();
     }

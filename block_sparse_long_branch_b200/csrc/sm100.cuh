@@ -444,6 +444,13 @@ __device__ __forceinline__ float max3f_ordered(float a, float b, float c) {
   return d;
 }
 
+// 32 bytes to global memory in one store (32-byte aligned)
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
@@ -483,6 +490,20 @@ __device__ __forceinline__ bool named_barrier_or(uint32_t id, uint32_t count, bo
       : "r"(pred ? 1u : 0u), "r"(id), "r"(count)
       : "memory");
   return r != 0;
+}
+
+// True in one lane of a converged warp (always the same one).  A branch on it is
+// known to the compiler to hold a single thread, which a test of the lane number
+// is not: tcgen05 instructions in it take their operands straight from uniform
+// registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok));
+  return ok != 0;
 }
 
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31u; }
