@@ -97,7 +97,7 @@ DecodeWs decode_ws(const msa_config_t* c, int32_t B) {
   w.tickets = off;
   off += align256((size_t)B * dense_decode_chunks(c->num_heads, c->num_groups) * 4);
   w.part = off;
-  off += (size_t)kMaxCtas * 2 *
+  off += (size_t)kMaxCtas * 2 * kDenseDecodeWarps *
          dense_decode_partial_floats(c->num_heads, c->num_groups, c->head_dim) * 4;
   w.total = off;
   return w;

@@ -2,16 +2,18 @@
 // paged cache:  out[b][h] = sum_{s < L_b} softmax_s(scale <q[b][h], k[s][g]>) v[s][g].
 //
 // Memory bound: 4 d bytes of K and V per (key, group) against 4 d (H/G) operations.
-// The keys of all (sequence, group) items are one line of 16-key steps, cut into
-// equal shares, one per CTA; an item that lies in several shares is joined from
-// their partial results by the CTA that finishes last, always in the order of
-// the shares, so results do not depend on timing.
+// The keys of all sequences are one line of 16-key steps (32 at d = 64), cut into
+// equal shares, one per CTA; what lies in several shares is joined from partial
+// results by whoever finishes last, always in the order of the shares, so results
+// do not depend on timing.
 //
-// In a CTA eight warps take an item's steps in turn.  Each warp has a ring of its
-// own in shared memory that its lane 0 fills by TMA (one copy of 16 rows of K and
-// one of V per step, never across a page), so the warps do not wait for one another
-// until an item ends.  A warp keeps the running maximum, sum and output of its
-// steps in registers:
+// The eight warps of a CTA take gw groups x 8/gw neighbouring steps at a time.
+// Where there is work enough gw is 8: the warps read whole rows of the cache
+// between them, and none waits for another.  A short line is cut finer with gw
+// down to 1, eight steps of one group at a time.  Each warp has a ring of its own
+// in shared memory that it fills by TMA (a copy of K and one of V per step, never
+// across a page), and keeps the running maximum, sum and output of its steps in
+// registers:
 //   S = Q K^T  mma.m16n8k16: the 16 rows are the group's heads (8 heads: rows 8-15
 //              are zero; 16 heads: all used)
 //   O += P V   P in two bf16 parts, hi = bf16(p) and lo = bf16(p - hi), so the
@@ -28,19 +30,22 @@
 namespace msa {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = kDenseDecodeWarps;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStep = 16;  // keys per step
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ROWS: head rows of an item (8 or 16)
 template <int D, int ROWS>
 struct DecodeCfg {
+  // keys per step: 8 KiB of K and V either way.  At d = 64 steps of 16 keys left a
+  // warp waiting on its own chain of instructions (decode_ragged: see below)
+  static constexpr int kStep = D == 128 ? 16 : 32;
   static constexpr int kHalf = kStep * D * 2;  // K or V of one step
   static constexpr int kStageBytes = 2 * kHalf;
   static constexpr int kJoin = kWarps * ROWS * D * 4;  // the warps' outputs of an item
   // what 224 KiB hold beside the join buffer: 3 stages of 8 KiB a warp for 8 heads of 128
   static constexpr int kStages = (224 * 1024 - kJoin) / (kWarps * kStageBytes);
+  static_assert(kWarps * kStages <= kThreads, "one thread per barrier");
   static constexpr int kSmem = kWarps * kStages * kStageBytes + kJoin + 1024;
   static constexpr int kPart = ROWS * (D + 2);  // floats of a partial
 };
@@ -88,14 +93,18 @@ __device__ __forceinline__ int seq_len(const Args& a, int b) {
   }
   return L;
 }
-__device__ __forceinline__ int n_steps(int L) { return (L + kStep - 1) / kStep; }
+template <int STEP>
+__device__ __forceinline__ int n_steps(int L) {
+  return (L + STEP - 1) / STEP;
+}
 
-// A position in the line of all steps: step `st` of item `item` of sequence b.
+// A position in the line: step `st` of bundle `bd` (gw neighbouring items) of sequence b.
 struct Cursor {
-  int b, item;     // item in [0, G*HC)
+  int b, bd;
   int L, n;        // length and steps of sequence b
-  int st;          // step within the item
-  int64_t left;    // steps from here to the end of the share
+  int st;          // step within the bundle
+  int steps;       // steps of this part, from st on
+  long long left;  // line positions from this part's first to the end of the share
 };
 
 template <int D, int ROWS>
@@ -103,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     dense_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const Args a) {
   using Cfg = DecodeCfg<D, ROWS>;
+  constexpr int kStep = Cfg::kStep;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -110,142 +120,189 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t bar_full[kWarps][Cfg::kStages];
   __shared__ float jm[kWarps][ROWS], jl[kWarps][ROWS];
   __shared__ long long red[kWarps];
-  __shared__ long long scan_base;
-  __shared__ int start_b;
   __shared__ long long start_off;
-  __shared__ int abort_s, last_s;
+  __shared__ int start_b, start_len;
+  __shared__ int abort_s, last_s[kWarps];
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
   const int items = a.G * a.HC;
+  if (tid < kWarps * Cfg::kStages) {
+    mbar_init(&bar_full[0][0] + tid, 1);
+    fence_mbar_init();
+  }
   if (tid == 0) {
     abort_s = 0;
-    for (int w = 0; w < kWarps; ++w)
-      for (int s = 0; s < Cfg::kStages; ++s) mbar_init(&bar_full[w][s], 1);
-    fence_mbar_init();
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
   }
-  // ---- the total number of steps, and this CTA's share ----
-  long long mine = 0;
-  for (int b = tid; b < a.B; b += kThreads) mine += n_steps(seq_len(a, b));
-  long long v = mine;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (lane == 0) red[warp] = v;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += red[w];
-  total *= items;
-  // a share is at least one step per warp, so that a short line is not spread thin
-  long long share = (total + gridDim.x - 1) / gridDim.x;
-  if (share < kWarps) share = kWarps;
-  const long long lo = share * blockIdx.x;
-  const long long hi = lo + share < total ? lo + share : total;
-  // empty sequences: zero rows
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    if (seq_len(a, b) == 0) {
-      uint4* o = reinterpret_cast<uint4*>(a.out + (int64_t)b * a.H * D);
-      for (int x = tid; x < a.H * D / 8; x += kThreads) o[x] = make_uint4(0, 0, 0, 0);
-    }
-  }
-  if (lo >= hi) return;
-  // ---- the sequence that holds step lo ----
-  if (tid == 0) scan_base = 0;
-  __syncthreads();
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    const long long n = b < a.B ? (long long)n_steps(seq_len(a, b)) * items : 0;
+  // ---- the number of steps of all sequences ----
+  // Sum over the block and this thread's exclusive prefix; up to 32 sequences
+  // every warp does it for itself.
+  const bool few = a.B <= 32;
+  auto prefix = [&](long long n, long long& before) {
     long long x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
+    before = x - n;
+    if (few) return __shfl_sync(0xffffffffu, x, 31);
+    __syncthreads();
     if (lane == 31) red[warp] = x;
     __syncthreads();
-    const long long base0 = scan_base;
-    long long base = base0;
-    for (int w = 0; w < warp; ++w) base += red[w];
-    const long long first = base + x - n;
-    if (lo >= first && lo < first + n) {
-      start_b = b;
-      start_off = lo - first;
-    }
     long long sum = 0;
-    for (int w = 0; w < kWarps; ++w) sum += red[w];
-    __syncthreads();
-    if (tid == 0) scan_base = base0 + sum;
-    __syncthreads();
-    if (base0 + sum > lo) break;
-  }
-
-  auto next_item = [&](Cursor& c) {
-    if (++c.item < items) return;
-    c.item = 0;
-    do {
-      ++c.b;
-      c.L = c.b < a.B ? seq_len(a, c.b) : 1;
-    } while (c.L == 0);
-    c.n = n_steps(c.L);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += red[w];
+      sum += red[w];
+    }
+    return sum;
   };
-  Cursor cur;  // of the part being computed: its first step
-  cur.b = start_b;
-  cur.L = seq_len(a, cur.b);
-  cur.n = n_steps(cur.L);
-  cur.item = (int)(start_off / cur.n);
-  cur.st = (int)(start_off % cur.n);
-  cur.left = hi - lo;
+  const int me = few ? lane : tid;  // the sequence of this thread, of 256 (32) at a time
+  long long total = 0, seqs = 0, before = 0;
+  int len = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const int b = b0 + me;
+    len = b < a.B ? seq_len(a, b) : 0;
+    if (b < a.B && len == 0 && b % (int)gridDim.x == (int)blockIdx.x && tid == me) {
+      // an empty sequence: zeros
+      uint4* o = reinterpret_cast<uint4*>(a.out + (int64_t)b * a.H * D);
+      for (int x = 0; x < a.H * D / 8; ++x) o[x] = make_uint4(0, 0, 0, 0);
+    }
+    // steps below 2^40, sequences above it: one sum for both
+    const long long sum = prefix((long long)n_steps<kStep>(len) + (len > 0 ? 1ll << 40 : 0), before);
+    total += sum & ((1ll << 40) - 1);
+    seqs += sum >> 40;
+  }
+  // ---- groups at a time, and the line ----
+  // gw: as many groups as divide the items evenly, while a share keeps 16 steps
+  int gw = (items & 7) == 0 ? 8 : (items & 3) == 0 ? 4 : (items & 1) == 0 ? 2 : 1;
+  while (gw > 1 && total * items < 16ll * gw * gridDim.x) gw >>= 1;
+  const int kw = kWarps / gw, bundles = items / gw;
+  const int gi = warp % gw, ki = warp / gw;  // this warp's group of the bundle, and its steps' offset
+  // A part costs about as much as 4 steps of each warp beside its steps (its
+  // queries' latency, the join, the output): so much longer is its bundle in the
+  // line.  Few bundles are padded to whole shares instead, so that no share holds
+  // the ends of two, which would take it twice the time.
+  const long long n_bundles = seqs * bundles;
+  const bool padded = n_bundles * 8 <= gridDim.x;
+  const int cost = padded ? 0 : 4 * kw;
+  const long long line = total * bundles + cost * n_bundles;
+  const long long ctas = padded ? gridDim.x - n_bundles : gridDim.x;
+  long long share = (line + ctas - 1) / ctas;
+  if (share < kw) share = kw;
+  auto length = [&](int n) -> long long {  // of a bundle of n steps in the line
+    if (n == 0) return 0;
+    return padded ? (n + share - 1) / share * share : (long long)n + cost;
+  };
+  const long long lo = share * blockIdx.x, hi = lo + share;
+  // ---- the sequence that holds position lo ----
+  {
+    long long base = 0;
+    bool found = false;
+    for (int b0 = 0; b0 < a.B && base <= lo; b0 += kThreads) {
+      const int b = b0 + me;
+      if (a.B > kThreads) len = b < a.B ? seq_len(a, b) : 0;
+      const long long mine = length(n_steps<kStep>(len)) * bundles;
+      const long long sum = prefix(mine, before);
+      before += base;
+      found = lo >= before && lo < before + mine;
+      if (found && tid == me) start_b = b, start_len = len, start_off = lo - before;
+      base += sum;
+    }
+    if (lo >= base) return;  // the line ends before this share: the same for all threads
+  }
+  __syncthreads();
+
+  // the part at line offset `off` of the cursor's bundle
+  auto set_part = [&](Cursor& c, long long off) {
+    const long long end = off + c.left;  // where the share ends
+    const long long s0 = off - cost, s1 = end - cost;
+    c.st = (int)(s0 < 0 ? 0 : s0);
+    const long long e = s1 < c.n ? s1 : c.n;
+    c.steps = e > c.st ? (int)(e - c.st) : 0;
+  };
+  auto next_part = [&](Cursor& c, long long used) {  // `used` line positions on: the next bundle
+    c.left -= used;
+    if (c.left <= 0) return;
+    if (++c.bd == bundles) {
+      c.bd = 0;
+      do {
+        if (++c.b >= a.B) {
+          c.left = 0;
+          return;
+        }
+        c.L = seq_len(a, c.b);
+      } while (c.L == 0);
+      c.n = n_steps<kStep>(c.L);
+    }
+    set_part(c, 0);
+  };
+  // line positions from the part's first to its bundle's end
+  long long cur_rest;
+  Cursor cur;
+  {
+    cur.b = start_b;
+    cur.L = start_len;
+    cur.n = n_steps<kStep>(cur.L);
+    const long long len1 = length(cur.n);
+    cur.bd = (int)(start_off / len1);
+    const long long off = start_off - cur.bd * len1;
+    cur.left = hi - lo;
+    set_part(cur, off);
+    cur_rest = len1 - off;
+  }
 
   // ---- this warp's loads: its steps of every part, in order ----
   uint8_t* ring = smem + warp * Cfg::kStages * Cfg::kStageBytes;
-  Cursor ld = cur;      // part that the next load belongs to
-  int ld_st = cur.st + warp;
+  Cursor ld = cur;  // part of the next load
+  long long ld_rest = cur_rest;
+  int ld_k = 0;     // this warp's number of the next step in its part
   uint32_t issued = 0, used = 0;
-  int page_next = 0;    // page id of the next load
-  auto part_end = [&](const Cursor& c) {
-    return (int)(c.left < (long long)(c.n - c.st) ? c.st + c.left : c.n);
-  };
-  // move `ld` to the part that holds this warp's next step; false at the end
-  auto settle = [&]() {
-    while (ld.left > 0) {
-      const int e = part_end(ld);
-      if (ld_st < e) {
-        page_next = __ldg(a.block_table + (int64_t)ld.b * a.table_stride +
-                          ld_st * kStep / a.page_size);
-        return true;
-      }
-      ld.left -= e - ld.st;
-      if (ld.left > 0) {
-        next_item(ld);
-        ld.st = 0;
-        ld_st = warp;
-      }
-    }
-    return false;
-  };
-  bool more = settle();
+  // a step lies in one page, or (32 keys in pages of 16) in two
+  const int box_rows = a.page_size < kStep ? a.page_size : kStep;
+  const int boxes = kStep / box_rows;
+  const int ahead = 32 / boxes;  // steps whose page ids one load of the warp brings
+  int pages = 0;                 // lane i: page of box i % boxes of step i / boxes of those
   auto load = [&]() {
-    if (!more) return;
+    while (ld.left > 0 && ki + ld_k * kw >= ld.steps) {
+      next_part(ld, ld_rest);
+      if (ld.left > 0) ld_rest = length(ld.n);
+      ld_k = 0;
+    }
+    if (ld.left <= 0) return;
+    if (ld_k % ahead == 0) {
+      const int st = ki + (ld_k + lane / boxes) * kw;
+      const int key = (ld.st + st) * kStep + lane % boxes * box_rows;
+      pages = 0;
+      if (st < ld.steps && key < ld.L)
+        pages = __ldg(a.block_table + (int64_t)ld.b * a.table_stride + key / a.page_size);
+    }
     const uint32_t s = issued % Cfg::kStages;
-    if (lane == 0) {
-      int pg = page_next;
+    const int key0 = (ld.st + ki + ld_k * kw) * kStep;
+    const int n = min(boxes, (ld.L - key0 + box_rows - 1) / box_rows);
+    int pg = __shfl_sync(0xffffffffu, pages, ld_k % ahead * boxes + lane % boxes);
+    if (lane == 0) mbar_arrive_expect_tx(&bar_full[warp][s], n * box_rows * D * 4);
+    __syncwarp();
+    if (lane < n) {
       if (pg < 0 || pg >= a.num_pages) {
         record_error(a.err, kDevBadIndex);
         pg = a.num_pages;  // outside the tensor: reads zeros
       }
-      const int row = ld_st * kStep % a.page_size;
-      uint8_t* dst = ring + s * Cfg::kStageBytes;
-      mbar_arrive_expect_tx(&bar_full[warp][s], Cfg::kStageBytes);
-      tma_load_5d(dst, &map_k, &bar_full[warp][s], 0, row, 0, ld.item / a.HC, pg);
-      tma_load_5d(dst + Cfg::kHalf, &map_v, &bar_full[warp][s], 0, row, 0, ld.item / a.HC, pg);
+      const int row = (key0 + lane * box_rows) % a.page_size;
+      const int g = (ld.bd * gw + gi) / a.HC;
+      uint8_t* dst = ring + s * Cfg::kStageBytes + lane * box_rows * 128;
+      tma_load_5d(dst, &map_k, &bar_full[warp][s], 0, row, 0, g, pg);
+      tma_load_5d(dst + Cfg::kHalf, &map_v, &bar_full[warp][s], 0, row, 0, g, pg);
     }
+    __syncwarp();
     ++issued;
-    ld_st += kWarps;
-    more = settle();
+    ++ld_k;
   };
 #pragma unroll 1
   for (int s = 0; s < Cfg::kStages; ++s) load();
 
+  constexpr int NT = kStep / 8;
   const int gq = lane >> 2, tq = lane & 3;
   const uint32_t ring_u = smem_u32(ring);
   // lane addresses within a step: K rows (lane & 7), 16-byte column lane >> 3;
@@ -254,8 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int v_r = (lane & 7) + ((lane >> 3) & 1) * 8, v_c = lane >> 4;
 
   while (cur.left > 0) {
-    const int end = part_end(cur);
-    const int g = cur.item / a.HC, h0 = (cur.item % a.HC) * ROWS;
+    const int item = cur.bd * gw + gi;
+    const int g = item / a.HC, h0 = item % a.HC * ROWS;
     const int nh = min(ROWS, a.HG - h0);
     // Q fragments: rows gq and gq + 8
     uint32_t qa[D / 16][ROWS / 4];
@@ -279,13 +336,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int rr = 0; rr < ROWS / 8; ++rr) m[rr] = -INFINITY, l[rr] = 0.f;
 
-    for (int st = cur.st + warp; st < end; st += kWarps) {
+    for (int st = ki; st < cur.steps; st += kw) {
       const uint32_t sg = used % Cfg::kStages;
       if (!mbar_wait(&bar_full[warp][sg], (used / Cfg::kStages) & 1, &abort_s, a.err,
                      kDevTimeoutLoad))
         break;
       const uint32_t kb = ring_u + sg * Cfg::kStageBytes, vb = kb + Cfg::kHalf;
-      const int valid = cur.L - st * kStep;  // keys of this step that exist
+      const int valid = cur.L - (cur.st + st) * kStep;  // keys of this step that exist
       if (valid < kStep) {
         // 128-byte lines, chunk-major; a line is one row's 64 columns
         uint4* vz = reinterpret_cast<uint4*>(ring + sg * Cfg::kStageBytes + Cfg::kHalf);
@@ -294,10 +351,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_async_smem();
         __syncwarp();
       }
-      // ---- S: two tiles of 8 keys ----
-      float s[2][4];
+      // ---- S: tiles of 8 keys; even and odd k-steps in sums of their own ----
+      float s[NT][4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < NT; ++t) {
+        float s2[4] = {0.f, 0.f, 0.f, 0.f};
         s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
 #pragma unroll
         for (int kp = 0; kp < D / 32; ++kp) {  // 32 dimensions: two k-steps
@@ -308,27 +366,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 2; ++x) {
             const int kk = 2 * kp + x;
             if (ROWS == 8)
-              mma_16816(s[t], qa[kk][0], 0u, qa[kk][1], 0u, b[2 * x], b[2 * x + 1]);
+              mma_16816(x ? s2 : s[t], qa[kk][0], 0u, qa[kk][1], 0u, b[2 * x], b[2 * x + 1]);
             else
-              mma_16816(s[t], qa[kk][0], qa[kk][1 % (ROWS / 4)], qa[kk][2 % (ROWS / 4)],
+              mma_16816(x ? s2 : s[t], qa[kk][0], qa[kk][1 % (ROWS / 4)], qa[kk][2 % (ROWS / 4)],
                         qa[kk][3 % (ROWS / 4)], b[2 * x], b[2 * x + 1]);
           }
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][e] += s2[e];
       }
       // ---- running maximum, P, sum ----
       float f[ROWS / 8];
-      float p[ROWS / 8][4];
+      float p[ROWS / 8][2 * NT];
       bool grew = false;
 #pragma unroll
       for (int rr = 0; rr < ROWS / 8; ++rr) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float x = s[t][2 * rr + e] * a.scale_log2;
             p[rr][2 * t + e] = t * 8 + 2 * tq + e < valid ? x : -INFINITY;
           }
-        float mx = fmaxf(fmaxf(p[rr][0], p[rr][1]), fmaxf(p[rr][2], p[rr][3]));
+        float mx = p[rr][0];
+#pragma unroll
+        for (int e = 1; e < 2 * NT; ++e) mx = fmaxf(mx, p[rr][e]);
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const float mn = fmaxf(m[rr], mx);
@@ -337,8 +399,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         grew |= mn > m[rr];
         m[rr] = mn;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[rr][e] = fast_exp2(p[rr][e] - mu);
-        l[rr] = l[rr] * f[rr] + ((p[rr][0] + p[rr][1]) + (p[rr][2] + p[rr][3]));
+        for (int e = 0; e < 2 * NT; ++e) p[rr][e] = fast_exp2(p[rr][e] - mu);
+        float ls = p[rr][0];
+#pragma unroll
+        for (int e = 1; e < 2 * NT; ++e) ls += p[rr][e];
+        l[rr] = l[rr] * f[rr] + ls;
       }
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -348,41 +413,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // ---- O += P V, P = hi + lo ----
-      uint32_t hi2[ROWS / 8][2], lo2[ROWS / 8][2];
+      uint32_t hi2[ROWS / 8][NT], lo2[ROWS / 8][NT];
 #pragma unroll
       for (int rr = 0; rr < ROWS / 8; ++rr)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < NT; ++t) {
           const uint32_t w = pack_bf16x2(p[rr][2 * t], p[rr][2 * t + 1]);
           hi2[rr][t] = w;
           lo2[rr][t] = pack_bf16x2(p[rr][2 * t] - __uint_as_float(w << 16),
                                    p[rr][2 * t + 1] - __uint_as_float(w & 0xFFFF0000u));
         }
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {  // 16 dimensions
-        uint32_t b[4];
-        const int col = 2 * i + v_c;
-        ldsm_x4_t(b, vb + (col >> 3) * (kStep * 128) + sw128_offset(v_r, col & 7));
+      for (int kt = 0; kt < NT / 2; ++kt)  // 16 keys
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (ROWS == 8) {
-            mma_16816(o[2 * i + x], hi2[0][0], lo2[0][0], hi2[0][1], lo2[0][1], b[2 * x],
-                      b[2 * x + 1]);
-          } else {
-            constexpr int R1 = ROWS / 8 - 1;
-            mma_16816(o[2 * i + x], hi2[0][0], hi2[R1][0], hi2[0][1], hi2[R1][1], b[2 * x],
-                      b[2 * x + 1]);
-            mma_16816(o[2 * i + x], lo2[0][0], lo2[R1][0], lo2[0][1], lo2[R1][1], b[2 * x],
-                      b[2 * x + 1]);
+        for (int i = 0; i < D / 16; ++i) {  // 16 dimensions
+          uint32_t b[4];
+          const int col = 2 * i + v_c;
+          ldsm_x4_t(b, vb + (col >> 3) * (kStep * 128) + sw128_offset(kt * 16 + v_r, col & 7));
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (ROWS == 8) {
+              mma_16816(o[2 * i + x], hi2[0][2 * kt], lo2[0][2 * kt], hi2[0][2 * kt + 1],
+                        lo2[0][2 * kt + 1], b[2 * x], b[2 * x + 1]);
+            } else {
+              constexpr int R1 = ROWS / 8 - 1;
+              mma_16816(o[2 * i + x], hi2[0][2 * kt], hi2[R1][2 * kt], hi2[0][2 * kt + 1],
+                        hi2[R1][2 * kt + 1], b[2 * x], b[2 * x + 1]);
+              mma_16816(o[2 * i + x], lo2[0][2 * kt], lo2[R1][2 * kt], lo2[0][2 * kt + 1],
+                        lo2[R1][2 * kt + 1], b[2 * x], b[2 * x + 1]);
+            }
           }
         }
-      }
       ++used;
       __syncwarp();  // every lane has read the stage
       load();
     }
 
-    // ---- join the warps ----
+    // ---- join the warps of a group; none to join when each has its own ----
+    // (warps gi, gi + gw, ...; the buffers are a warp's own)
+    auto sync = [&]() {
+      if (kw == 1)
+        __syncwarp();
+      else
+        __syncthreads();
+    };
     if (ROWS == 8) {
       // lo products are in rows 8-15 of the same head
 #pragma unroll
@@ -394,85 +468,97 @@ __global__ void __launch_bounds__(kThreads, 1)
       l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 2);
       const int h = rr * 8 + gq;
       if (tq == 0) jm[warp][h] = m[rr], jl[warp][h] = l[rr];
-      float* dst = join + ((int64_t)warp * ROWS + h) * D + 2 * tq;
+      float* dst = join + (warp * ROWS + h) * D + 2 * tq;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
         *reinterpret_cast<float2*>(dst + i * 8) = make_float2(o[i][2 * rr], o[i][2 * rr + 1]);
     }
-    __syncthreads();
-    const bool whole = cur.st == 0 && end == cur.n;
-    // slot 0: the item began in an earlier share; 1: it begins in this one
-    float* part = a.part + ((int64_t)blockIdx.x * 2 + (cur.st > 0 ? 0 : 1)) * Cfg::kPart;
+    sync();
+    const int tg = ki * 32 + lane, n_tg = kw * 32;  // thread of the group's warps
+    const bool whole = cur.steps == cur.n;
+    // slot 0: the bundle began in an earlier share; 1: it begins in this one
+    float* part = a.part + (((int64_t)blockIdx.x * 2 + (cur.st > 0 ? 0 : 1)) * kWarps + gi) * Cfg::kPart;
     __nv_bfloat16* orow = a.out + ((int64_t)cur.b * a.H + g * a.HG + h0) * D;
-    for (int x = tid; x < nh * (D / 4); x += kThreads) {
-      const int h = x / (D / 4), c = x % (D / 4);
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, jm[w][h]);
-      const float Mu = M > -INFINITY ? M : 0.f;
-      float L = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = fast_exp2(jm[w][h] - Mu);
-        const float4 y = *reinterpret_cast<const float4*>(join + ((int64_t)w * ROWS + h) * D + 4 * c);
-        L += f * jl[w][h];
-        acc.x += f * y.x, acc.y += f * y.y, acc.z += f * y.z, acc.w += f * y.w;
-      }
-      if (whole) {
-        const float inv = 1.f / L;
-        *reinterpret_cast<uint2*>(orow + (int64_t)h * D + 4 * c) = make_uint2(
-            pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-      } else {
-        *reinterpret_cast<float4*>(part + h * D + 4 * c) = acc;
-        if (c == 0) part[ROWS * D + 2 * h] = M, part[ROWS * D + 2 * h + 1] = L;
-      }
-    }
-    if (!whole) {
-      // shares that hold parts of this item
-      const long long at = hi - cur.left;  // line position of this part
-      const long long first = at - cur.st, last = first + cur.n - 1;
-      const int c_first = (int)(first / share), c_last = (int)(last / share);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0)
-        last_s = atomicAdd(a.tickets + (int64_t)cur.b * items + cur.item, 1) == c_last - c_first;
-      __syncthreads();
-      if (last_s) {
-        __threadfence();
-        for (int x = tid; x < nh * (D / 4); x += kThreads) {
-          const int h = x / (D / 4), c = x % (D / 4);
-          auto at_part = [&](int z) {
-            return a.part + ((int64_t)z * 2 + (z == c_first ? 1 : 0)) * Cfg::kPart;
-          };
-          float M = -INFINITY;
-#pragma unroll 4
-          for (int z = c_first; z <= c_last; ++z)
-            M = fmaxf(M, __ldcg(at_part(z) + ROWS * D + 2 * h));
-          const float Mu = M > -INFINITY ? M : 0.f;
-          float L = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int z = c_first; z <= c_last; ++z) {
-            const float* pz = at_part(z);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pz + ROWS * D + 2 * h));
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(pz + h * D + 4 * c));
-            const float f = fast_exp2(ml.x - Mu);
-            L += f * ml.y;
-            acc.x += f * y.x, acc.y += f * y.y, acc.z += f * y.z, acc.w += f * y.w;
-          }
+    if (cur.steps > 0) {
+      for (int x = tg; x < nh * (D / 4); x += n_tg) {
+        const int h = x / (D / 4), c = x % (D / 4);
+        float M = -INFINITY;
+        for (int w = gi; w < kWarps; w += gw) M = fmaxf(M, jm[w][h]);
+        const float Mu = M > -INFINITY ? M : 0.f;
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = gi; w < kWarps; w += gw) {
+          const float f = fast_exp2(jm[w][h] - Mu);
+          const float4 y = *reinterpret_cast<const float4*>(join + (w * ROWS + h) * D + 4 * c);
+          L += f * jl[w][h];
+          acc.x += f * y.x, acc.y += f * y.y, acc.z += f * y.z, acc.w += f * y.w;
+        }
+        if (whole) {
           const float inv = 1.f / L;
           *reinterpret_cast<uint2*>(orow + (int64_t)h * D + 4 * c) = make_uint2(
               pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        } else {
+          *reinterpret_cast<float4*>(part + h * D + 4 * c) = acc;
+          if (c == 0) *reinterpret_cast<float2*>(part + ROWS * D + 2 * h) = make_float2(M, L);
+        }
+      }
+      if (!whole) {
+        // the shares that hold steps of this bundle
+        const long long at = hi - cur.left;                 // the part's line position
+        const long long first = at + cur_rest - length(cur.n) + cost;  // of step 0
+        const int c_first = (int)(first / share), c_last = (int)((first + cur.n - 1) / share);
+        __threadfence();
+        sync();
+        if (tg == 0)
+          last_s[gi] =
+              atomicAdd(a.tickets + (int64_t)cur.b * items + item, 1) == c_last - c_first;
+        sync();
+        if (last_s[gi]) {
+          __threadfence();
+          for (int x = tg; x < nh * (D / 4); x += n_tg) {
+            const int h = x / (D / 4), c = x % (D / 4);
+            // 8 parts at a time, all their loads in flight together
+            float M = -INFINITY, L = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int z0 = c_first; z0 <= c_last; z0 += 8) {
+              float2 ml[8];
+              float4 y[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int z = z0 + i <= c_last ? z0 + i : c_last;
+                const float* pz =
+                    a.part + (((int64_t)z * 2 + (z == c_first ? 1 : 0)) * kWarps + gi) * Cfg::kPart;
+                ml[i] = __ldcg(reinterpret_cast<const float2*>(pz + ROWS * D + 2 * h));
+                y[i] = __ldcg(reinterpret_cast<const float4*>(pz + h * D + 4 * c));
+              }
+              float mn = M;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) mn = fmaxf(mn, ml[i].x);
+              const float mu = mn > -INFINITY ? mn : 0.f;
+              const float f0 = fast_exp2(M - mu);
+              L *= f0;
+              acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (z0 + i <= c_last) {
+                  const float f = fast_exp2(ml[i].x - mu);
+                  L += f * ml[i].y;
+                  acc.x += f * y[i].x, acc.y += f * y[i].y;
+                  acc.z += f * y[i].z, acc.w += f * y[i].w;
+                }
+              }
+              M = mn;
+            }
+            const float inv = 1.f / L;
+            *reinterpret_cast<uint2*>(orow + (int64_t)h * D + 4 * c) = make_uint2(
+                pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          }
         }
       }
     }
-    __syncthreads();  // join, jm, jl are reused by the next part
-    cur.left -= end - cur.st;
-    if (cur.left > 0) {
-      next_item(cur);
-      cur.st = 0;
-    }
+    sync();  // the buffers are reused by the next part
+    next_part(cur, cur_rest);
+    if (cur.left > 0) cur_rest = length(cur.n);
   }
   if (abort_s) {
     // copies in flight must land before the CTA's shared memory goes
@@ -490,7 +576,8 @@ cudaError_t launch_impl(const DenseDecodeLaunch& p, cudaStream_t s) {
   const uint64_t dims[5] = {64, (uint64_t)p.cache.page_size, D / 64, (uint64_t)p.G,
                             (uint64_t)p.cache.num_pages};
   const uint64_t str[4] = {GD, 64, D, (uint64_t)p.cache.page_stride};
-  const uint32_t box[5] = {64, kStep, D / 64, 1, 1};
+  const uint32_t box_rows = p.cache.page_size < Cfg::kStep ? p.cache.page_size : Cfg::kStep;
+  const uint32_t box[5] = {64, box_rows, D / 64, 1, 1};
   if (!make_tmap_bf16_nd(&mk, p.cache.k, 5, dims, str, box) ||
       !make_tmap_bf16_nd(&mv, p.cache.v, 5, dims, str, box))
     return cudaErrorInvalidValue;

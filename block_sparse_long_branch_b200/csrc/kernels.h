@@ -268,10 +268,11 @@ struct DenseDecodeLaunch {
   float scale;
   void* out;         // [B][H][d]
   int32_t* tickets;  // [B][head chunks], zero at launch
-  float* part;       // [grid][2][dense_decode_partial_floats()]
+  float* part;       // [grid][2][kDenseDecodeWarps][dense_decode_partial_floats()]
   uint32_t* err;
   int grid;
 };
+constexpr int kDenseDecodeWarps = 8;
 int dense_decode_chunks(int H, int G);  // (group, heads) items per sequence
 size_t dense_decode_partial_floats(int H, int G, int d);
 cudaError_t launch_dense_decode(const DenseDecodeLaunch& p, cudaStream_t s);

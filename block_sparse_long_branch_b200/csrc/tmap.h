@@ -75,6 +75,8 @@ inline bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t d0, u
 
 // bf16 view of `rank` (3 to 5) dimensions: extents `dims` (innermost first),
 // element strides `strides` of dimensions 1 .. rank-1, box `box`; 128-byte swizzle.
+// L2 fetches the 128 bytes a box's line asks for, not 256: a line's neighbour
+// belongs to another head, read at another time.
 inline bool make_tmap_bf16_nd(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                               const uint64_t* strides, const uint32_t* box) {
   auto enc = tensor_map_encoder();
@@ -89,7 +91,7 @@ inline bool make_tmap_bf16_nd(CUtensorMap* map, const void* base, int rank, cons
   }
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, st, b,
                    estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

@@ -68,10 +68,10 @@ def prefill_varlen(q, k, v, cu, scale):
 
 
 def paged_rows(cache, table_row, L) -> np.ndarray:
-    """Rows 0..L-1 of one sequence, token by token."""
+    """Rows 0..L-1 of one sequence of an fp64 cache."""
     page = cache.shape[1]
-    rows = [as_f64(cache[int(table_row[p // page]), p % page]) for p in range(0, L)]
-    return np.stack(rows) if rows else np.zeros((0,) + tuple(cache.shape[2:]))
+    p = np.arange(L)
+    return cache[np.asarray(table_row)[p // page], p % page]
 
 
 def prefill_paged(q, k_cache, v_cache, table, cu, seq_lens, scale):

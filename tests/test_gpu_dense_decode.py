@@ -65,6 +65,18 @@ def test_many_sequences(msa):
     run(msa, 4, 1, 64, 16, lens)
 
 
+@pytest.mark.parametrize("H,G,d,lens", [
+    (16, 8, 128, [9000, 1, 17, 12000, 0, 400, 16000, 33, 2]),  # all eight groups at a time
+    (10, 2, 64, [30000, 5, 20001]),                            # two
+    (32, 1, 64, [40000, 100]),                                 # two chunks of 16 heads
+    (12, 4, 128, [8000, 31000, 3]),                            # four
+    (3, 3, 128, [25000, 16, 7000]),                            # one
+])
+def test_long_lines(msa, H, G, d, lens):
+    """Enough steps that several groups are read at a time and shares end inside sequences."""
+    run(msa, H, G, d, 64, lens, side_by_side=True)
+
+
 def test_one_long_sequence_of_one_group(msa):
     """6000 keys of a single item: every CTA holds a share."""
     run(msa, 8, 1, 64, 32, [6000])
