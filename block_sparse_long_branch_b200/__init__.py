@@ -604,7 +604,7 @@ def msa_decode_static(cfg: MsaConfig, q, q_idx, k_cache, v_cache, k_idx_cache, c
 class PagedKV:
     """A paged cache and the block table of one batch (see ``paged_kv``)."""
 
-    __slots__ = ("k", "v", "block_table", "device", "batch", "heads", "dim", "struct", "ref")
+    __slots__ = ("k", "v", "block_table", "index", "batch", "heads", "dim", "struct", "ref")
 
     def __init__(self, k, v, block_table):
         for name, t in (("k_cache", k), ("v_cache", v)):
@@ -630,7 +630,7 @@ class PagedKV:
             raise ValueError("block_table must live on the cache's device")
         table = _dev(block_table, torch.int32, "block_table")
         self.k, self.v, self.block_table = k, v, block_table
-        self.device, self.batch, self.heads, self.dim = k.device, block_table.shape[0], G, d
+        self.index, self.batch, self.heads, self.dim = k.get_device(), block_table.shape[0], G, d
         self.struct = _PagedKVStruct(k.data_ptr(), v.data_ptr(), table, pages, stride, page_size,
                                      block_table.shape[1])
         self.ref = ctypes.byref(self.struct)
@@ -643,79 +643,82 @@ def paged_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Te
     return PagedKV(k_cache, v_cache, block_table)
 
 
-def _on(t, device, name: str) -> None:
-    if t.device != device:
-        raise ValueError(f"{name} lives on {t.device}, expected {device}")
+def _arg(t, dtype, shape, index: int, name: str) -> int:
+    """Pointer of a contiguous tensor of the given type, shape and device number."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == index and t.is_contiguous()):
+        return t.data_ptr()
+    _same_device(t, index, name)
+    return _dev(t, dtype, name, shape).value  # says what is wrong
 
 
-def _rows(t, name: str, T: int, heads: int, d: int, device) -> Tuple[int, int]:
-    """Pointer and row stride of a [T, heads, d] tensor with contiguous rows."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != (T, heads, d):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, heads, d)}")
-    if t.device != device:
-        raise ValueError(f"{name} lives on {t.device}, expected {device}")
-    st = t.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != d):
+def _same_device(t, index: int, name: str) -> None:
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != index:
+        raise ValueError(f"{name} lives on {t.device}, expected cuda:{index}")
+
+
+def _rows(t, name: str, shape, index: int) -> Tuple[int, int]:
+    """Pointer and row stride of a [T, heads, d] bf16 tensor with contiguous rows."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == shape
+            and t.get_device() == index):
+        return _arg(t, torch.bfloat16, shape, index, name), 0
+    row, head, one = t.stride()
+    T, heads, d = shape
+    if one != 1 or (head != d and heads > 1):
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.data_ptr(), st[0] if T > 1 else heads * d
+    return t.data_ptr(), row if T > 1 else heads * d
 
 
-class _Call:
-    """Device, stream and scratch of one full-attention call.  Tensors that the binding allocates
-    on a stream other than the current one are kept from reuse until that stream is done."""
-
-    __slots__ = ("device", "stream", "other", "guard")
-
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError("the tensors must live on a CUDA device")
-        current = torch.cuda.current_stream(device)
-        if stream is None:
-            stream = current
-        elif stream.device != device:
-            raise ValueError(f"stream of {stream.device} for tensors on {device}")
-        self.device = device
-        self.stream = stream
-        self.other = stream.cuda_stream != current.cuda_stream
-        self.guard = None
-
-    def empty(self, shape, dtype):
-        if not self.other:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.stream):  # first use is on that stream
-            return torch.empty(shape, dtype=dtype, device=self.device)
-
-    def workspace(self, ws, cfg, op, T, B):
-        if ws is None:
-            return self.empty((msa_workspace_size(cfg, op, T, B),), torch.uint8)
-        if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != self.device:
-            raise ValueError(f"workspace must be a contiguous uint8 tensor on {self.device}")
-        return ws
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+def _place(t, stream):
+    """Device number, raw stream, and the stream itself when it is not the current one: what the
+    binding then allocates is allocated on it, so that the memory is not reused before the stream
+    is done with it."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("the tensors must live on a CUDA device")
+    index = t.get_device()
+    current = torch._C._cuda_getCurrentRawStream(index)
+    if stream is None:
+        return index, current, None
+    if stream.device_index != index:
+        raise ValueError(f"stream of {stream.device} for tensors on cuda:{index}")
+    raw = stream.cuda_stream
+    return index, raw, None if raw == current else stream
 
 
-def _kv_check(cfg: MsaConfig, kv: PagedKV, B: int, device) -> None:
+def _empty(shape, like, side, dtype=torch.bfloat16):
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(side):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _scratch(ws, cfg, op, T, B, like, side):
+    if ws is None:
+        return _empty((msa_workspace_size(cfg, op, T, B),), like, side, torch.uint8)
+    if ws.dtype is not torch.uint8 or not ws.is_contiguous() or ws.get_device() != like.get_device():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {like.device}")
+    return ws
+
+
+def _launch(fn, index: int, where: str, *args) -> None:
+    """The library call, on the tensors' device."""
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args)
+    if st != 0:
+        raise MsaError(st, where)
+
+
+def _kv_check(cfg: MsaConfig, kv: PagedKV, B: int, index: int) -> None:
     if not isinstance(kv, PagedKV):
         raise TypeError("the cache must be a PagedKV (see paged_kv)")
     if kv.heads != cfg.num_groups or kv.dim != cfg.head_dim:
         raise ValueError(f"the cache has {kv.heads} heads of {kv.dim}, expected {cfg.num_groups} "
                          f"of {cfg.head_dim}")
-    if kv.device != device:
-        raise ValueError(f"the cache lives on {kv.device}, expected {device}")
+    if kv.index != index:
+        raise ValueError(f"the cache lives on {kv.k.device}, expected cuda:{index}")
     if kv.batch != B:
         raise ValueError(f"the block table has {kv.batch} rows, expected {B}")
 
@@ -730,33 +733,31 @@ def msa_rope_append_paged(cfg: MsaConfig, q, k, v, inv_freq, kv: PagedKV, cu_seq
     [B] on the device (see include/msa.h).  Returns the rotated queries [T,H,d] (``q_out``, which
     may be a contiguous ``q`` itself), or None when ``q`` is None."""
     lib = load_library()
-    T, dev = k.shape[0], k.device
+    index, raw, side = _place(k, stream)
+    T = k.shape[0]
     H, G, d = cfg.num_heads, cfg.num_groups, cfg.head_dim
     B = seq_lens.shape[0]
-    call = _Call(dev, stream)
-    _kv_check(cfg, kv, B, dev)
-    kp, ks = _rows(k, "k", T, G, d, dev)
-    vp, vs = _rows(v, "v", T, G, d, dev)
+    _kv_check(cfg, kv, B, index)
+    kp, ks = _rows(k, "k", (T, G, d), index)
+    vp, vs = _rows(v, "v", (T, G, d), index)
     qp, qs, op = None, 0, None
     if q is not None:
-        qp, qs = _rows(q, "q", T, H, d, dev)
+        qp, qs = _rows(q, "q", (T, H, d), index)
         if q_out is None:
-            q_out = call.empty((T, H, d), torch.bfloat16)
-        _on(q_out, dev, "q_out")
-        op = _dev(q_out, torch.bfloat16, "q_out", (T, H, d))
+            q_out = _empty((T, H, d), k, side)
+            op = q_out.data_ptr()
+        else:
+            op = _arg(q_out, torch.bfloat16, (T, H, d), index, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    for t, name in ((inv_freq, "inv_freq"), (cu_seqlens, "cu_seqlens"), (seq_lens, "seq_lens")):
-        _on(t, dev, name)
-    ws = call.workspace(workspace, cfg, OP_ROPE_APPEND, T, B)
-    with call:
-        st = lib.msa_rope_append_paged(
-            ctypes.byref(cfg), qp, qs, kp, ks, vp, vs, _dev(inv_freq, torch.float32, "inv_freq"),
-            2 * inv_freq.numel(), 1 if interleaved else 0, kv.ref,
-            _dev(cu_seqlens, torch.int64, "cu_seqlens", (B + 1,)),
-            _dev(seq_lens, torch.int32, "seq_lens", (B,)), B, T, op, ws.data_ptr(), ws.numel(),
-            call.stream.cuda_stream)
-    _check(st, "msa_rope_append_paged")
+    nf = inv_freq.shape[0]
+    ws = _scratch(workspace, cfg, OP_ROPE_APPEND, T, B, k, side)
+    _launch(lib.msa_rope_append_paged, index, "msa_rope_append_paged", ctypes.byref(cfg), qp, qs,
+            kp, ks, vp, vs, _arg(inv_freq, torch.float32, (nf,), index, "inv_freq"), 2 * nf,
+            1 if interleaved else 0, kv.ref,
+            _arg(cu_seqlens, torch.int64, (B + 1,), index, "cu_seqlens"),
+            _arg(seq_lens, torch.int32, (B,), index, "seq_lens"), B, T, op, ws.data_ptr(),
+            ws.numel(), raw)
     return q_out
 
 
@@ -766,29 +767,23 @@ def msa_dense_prefill_varlen(cfg: MsaConfig, q, k, v, cu_seqlens,
     """Full causal attention of whole prompts packed along the token axis: q [T,H,d], k/v [T,G,d],
     host ``cu_seqlens`` (any int sequence of B+1 offsets).  Returns out [T,H,d]."""
     lib = load_library()
-    import numpy as _np
-    cu = _np.ascontiguousarray(_np.asarray(
-        cu_seqlens.cpu() if isinstance(cu_seqlens, torch.Tensor) else cu_seqlens,
-        dtype=_np.int64))
+    if hasattr(cu_seqlens, "tolist"):  # a tensor or an array
+        cu_seqlens = cu_seqlens.tolist()
+    cu = (ctypes.c_int64 * len(cu_seqlens))(*cu_seqlens)
     B = len(cu) - 1
-    T, dev = q.shape[0], q.device
+    index, raw, side = _place(q, stream)
+    T = q.shape[0]
     H, G, d = cfg.num_heads, cfg.num_groups, cfg.head_dim
-    if B < 1 or int(cu[-1]) != T:
+    if B < 1 or cu[B] != T:
         raise ValueError(f"cu_seqlens must end at the packed length {T}")
-    call = _Call(dev, stream)
-    for t, name in ((k, "k"), (v, "v")):
-        _on(t, dev, name)
+    bf = torch.bfloat16
     if out is None:
-        out = call.empty((T, H, d), torch.bfloat16)
-    _on(out, dev, "out")
-    ws = call.workspace(workspace, cfg, OP_DENSE_PREFILL, T, B)
-    with call:
-        st = lib.msa_dense_prefill_varlen(
-            ctypes.byref(cfg), _dev(q, torch.bfloat16, "q", (T, H, d)),
-            _dev(k, torch.bfloat16, "k", (T, G, d)), _dev(v, torch.bfloat16, "v", (T, G, d)),
-            cu.ctypes.data, B, _dev(out, torch.bfloat16, "out", (T, H, d)), ws.data_ptr(),
-            ws.numel(), call.stream.cuda_stream)
-    _check(st, "msa_dense_prefill_varlen")
+        out = _empty((T, H, d), q, side)
+    ws = _scratch(workspace, cfg, OP_DENSE_PREFILL, T, B, q, side)
+    _launch(lib.msa_dense_prefill_varlen, index, "msa_dense_prefill_varlen", ctypes.byref(cfg),
+            _arg(q, bf, (T, H, d), index, "q"), _arg(k, bf, (T, G, d), index, "k"),
+            _arg(v, bf, (T, G, d), index, "v"), cu, B, _arg(out, bf, (T, H, d), index, "out"),
+            ws.data_ptr(), ws.numel(), raw)
     return out
 
 
@@ -800,25 +795,19 @@ def msa_dense_prefill_paged(cfg: MsaConfig, q, kv: PagedKV, cu_seqlens, seq_lens
     the device, as for msa_rope_append_paged.  Returns out [T,H,d]; rows behind the last sequence
     are left as they were."""
     lib = load_library()
-    T, dev = q.shape[0], q.device
+    index, raw, side = _place(q, stream)
+    T = q.shape[0]
     H, d = cfg.num_heads, cfg.head_dim
     B = seq_lens.shape[0]
-    call = _Call(dev, stream)
-    _kv_check(cfg, kv, B, dev)
-    for t, name in ((cu_seqlens, "cu_seqlens"), (seq_lens, "seq_lens")):
-        _on(t, dev, name)
+    _kv_check(cfg, kv, B, index)
     if out is None:
-        out = call.empty((T, H, d), torch.bfloat16)
-    _on(out, dev, "out")
-    ws = call.workspace(workspace, cfg, OP_DENSE_PREFILL_PAGED, T, B)
-    with call:
-        st = lib.msa_dense_prefill_paged(
-            ctypes.byref(cfg), _dev(q, torch.bfloat16, "q", (T, H, d)), kv.ref,
-            _dev(cu_seqlens, torch.int64, "cu_seqlens", (B + 1,)),
-            _dev(seq_lens, torch.int32, "seq_lens", (B,)), B, T,
-            _dev(out, torch.bfloat16, "out", (T, H, d)), ws.data_ptr(), ws.numel(),
-            call.stream.cuda_stream)
-    _check(st, "msa_dense_prefill_paged")
+        out = _empty((T, H, d), q, side)
+    ws = _scratch(workspace, cfg, OP_DENSE_PREFILL_PAGED, T, B, q, side)
+    _launch(lib.msa_dense_prefill_paged, index, "msa_dense_prefill_paged", ctypes.byref(cfg),
+            _arg(q, torch.bfloat16, (T, H, d), index, "q"), kv.ref,
+            _arg(cu_seqlens, torch.int64, (B + 1,), index, "cu_seqlens"),
+            _arg(seq_lens, torch.int32, (B,), index, "seq_lens"), B, T,
+            _arg(out, torch.bfloat16, (T, H, d), index, "out"), ws.data_ptr(), ws.numel(), raw)
     return out
 
 
@@ -829,22 +818,17 @@ def msa_dense_decode_paged(cfg: MsaConfig, q, kv: PagedKV, seq_lens,
     and value are in it); ``seq_lens`` int32 [B] on the device.  Returns out [B,H,d], zeros for a
     sequence of length 0."""
     lib = load_library()
-    B, dev = q.shape[0], q.device
+    index, raw, side = _place(q, stream)
+    B = q.shape[0]
     H, d = cfg.num_heads, cfg.head_dim
-    call = _Call(dev, stream)
-    _kv_check(cfg, kv, B, dev)
-    _on(seq_lens, dev, "seq_lens")
+    _kv_check(cfg, kv, B, index)
     if out is None:
-        out = call.empty((B, H, d), torch.bfloat16)
-    _on(out, dev, "out")
-    ws = call.workspace(workspace, cfg, OP_DENSE_DECODE, B, B)
-    with call:
-        st = lib.msa_dense_decode_paged(
-            ctypes.byref(cfg), _dev(q, torch.bfloat16, "q", (B, H, d)), kv.ref,
-            _dev(seq_lens, torch.int32, "seq_lens", (B,)), B,
-            _dev(out, torch.bfloat16, "out", (B, H, d)), ws.data_ptr(), ws.numel(),
-            call.stream.cuda_stream)
-    _check(st, "msa_dense_decode_paged")
+        out = _empty((B, H, d), q, side)
+    ws = _scratch(workspace, cfg, OP_DENSE_DECODE, B, B, q, side)
+    _launch(lib.msa_dense_decode_paged, index, "msa_dense_decode_paged", ctypes.byref(cfg),
+            _arg(q, torch.bfloat16, (B, H, d), index, "q"), kv.ref,
+            _arg(seq_lens, torch.int32, (B,), index, "seq_lens"), B,
+            _arg(out, torch.bfloat16, (B, H, d), index, "out"), ws.data_ptr(), ws.numel(), raw)
     return out
 
 

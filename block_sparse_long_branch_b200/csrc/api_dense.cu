@@ -69,8 +69,8 @@ struct PrefillWs {
 PrefillWs prefill_ws(const msa_config_t* c, int64_t T, int32_t B, bool paged) {
   PrefillWs w;
   const int64_t U = 2 * dense_tile_tokens(c->num_heads, c->num_groups);
-  // a unit is split into parts of at least four key tiles, so packed prompts
-  // of up to four tiles never are
+  // a unit is split only when it has more than four key tiles, so packed prompts
+  // of up to 512 tokens never are
   w.max_slots = paged || T > 4 * 128 ? 2 * kMaxCtas : 0;
   w.max_units = (int32_t)(T / U + B + w.max_slots);
   size_t off = kHeader;
@@ -214,7 +214,6 @@ msa_status_t msa_dense_prefill_varlen(const msa_config_t* cfg, const void* q, co
   if (!ws || !aligned16(ws) || ws_bytes < prefill_ws(cfg, T, B, false).total)
     return MSA_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), s) != cudaSuccess) return cuda_status(cudaErrorUnknown);
   const size_t hd = (size_t)cfg->num_heads * cfg->head_dim * 2;
   const size_t gd = (size_t)cfg->num_groups * cfg->head_dim * 2;
   int launches = 0;
@@ -233,6 +232,7 @@ msa_status_t msa_dense_prefill_varlen(const msa_config_t* cfg, const void* q, co
     p.offsets = &off;
     p.B = n;
     p.T = rows;
+    p.clear_err = launches == 0;
     PrefillWs w = prefill_ws(cfg, rows, n, false);
     st = run_prefill(cfg, p, w, ws, s, &launches);
   }
@@ -257,7 +257,7 @@ msa_status_t msa_dense_prefill_paged(const msa_config_t* cfg, const void* q,
   const PrefillWs w = prefill_ws(cfg, T, B, true);
   if (!ws || !aligned16(ws) || ws_bytes < w.total) return MSA_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), s) != cudaSuccess) return cuda_status(cudaErrorUnknown);
+  p.clear_err = 1;
   static const DenseOffsets kNoOffsets = {};
   p.q = q;
   p.out = out;

@@ -29,12 +29,16 @@
 //
 // Warp roles (384 threads, one CTA per SM, persistent over the units):
 //   WG0, WG1  softmax of row tile 0 / 1, one thread per row; the rescaling of
-//             O; the final O / l;
-//   WG2       warp 8 TMA loads, warp 9 MMA issuer (one thread), warps 10, 11
-//             cleaning of V.
+//             O; the cleaning of V; the final O / l;
+//   WG2       warp 8 TMA loads, warp 9 MMA issuer (two warps idle: the register
+//             split goes by warpgroups).
 // TMEM (512 columns): S0, S1 (fp32; each P overwrites the first half of its S)
 // and O0, O1.  While one tile's exponentials are computed the tensor cores work
 // on the other tile.
+#include <algorithm>
+#include <type_traits>
+#include <utility>
+
 #include "kernels.h"
 #include "sm100.cuh"
 #include "tmap.h"
@@ -43,15 +47,14 @@ namespace msa {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kCleanWarp0 = 10;
-constexpr int kCleanThreads = 64;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr uint32_t kRegSoftmax = 208, kRegOther = 88;
 constexpr int kLaunchRegs = 168;  // 2*128*208 + 128*88 = 384*168
 constexpr int kRows = 128, kKeys = 128;
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;  // log2 of the growth of the maximum left unapplied
-constexpr int kFlagSlots = 4;
+constexpr int kFlagSlots = 8;
 
 template <int D>
 struct PrefillCfg {
@@ -80,8 +83,9 @@ struct Ring {
 struct PrefillArgs {
   int32_t H, G, HG, TT;
   float scale, scale_log2;
-  const DenseUnit* units;
-  const int32_t* n_units;  // tile pairs (each for all groups)
+  const DenseUnit* units;  // device plan: the units (each for all groups) and their number
+  const int32_t* n_units;
+  int32_t max_units;
   // paged keys and values; page_size 0: packed rows
   const int32_t* block_table;
   int32_t table_stride, page_size, num_pages;
@@ -90,29 +94,60 @@ struct PrefillArgs {
   __nv_bfloat16* out;
   float* part_o;     // [slot][256][D]
   float2* part_ml;   // [slot][256] (log2-domain maximum, sum)
+  int32_t clear_err;
   uint32_t* err;
 };
+
+// The units of a small batch whose lengths the host knows travel as a kernel
+// parameter: no planning kernel in front (prefill of 128 tokens: 14.4 -> 8.5 us).
+constexpr int kHostUnits = 128;
+struct HostUnits {
+  int32_t n;
+  DenseUnit u[kHostUnits];
+};
+struct HostSplits {
+  int32_t n;
+  DenseSplit s[kHostUnits / 2];
+};
+struct NoHostUnits {};
 
 struct Unit {
   DenseUnit d;
   int g;
-  int c0, c1;   // key tiles of row tile 0 / 1
   int nt;       // key tiles of the unit
+  int c0, c1;   // of these, taken by row tile 0 / 1
+  // A unit of one row tile is taken by both softmax warpgroups: "tile" i holds
+  // the same rows and takes every other key tile, from i on.
+  bool dual;
 };
 
 // The r-th unit of this CTA: units come longest first, and every other round
 // runs through the CTAs backwards, so that no CTA always gets the longer ones.
-__device__ __forceinline__ bool get_unit(const PrefillArgs& a, int total, int r, Unit& u) {
-  const int c = (r & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
-  const int64_t x = (int64_t)r * gridDim.x + c;
-  if (x >= total) return false;
-  const int i = (int)(x / a.G);
-  u.g = (int)(x - (int64_t)i * a.G);
-  const int4* p = reinterpret_cast<const int4*>(a.units + i);
-  const int4 x0 = __ldg(p), x1 = __ldg(p + 1);
-  u.d.tok0 = x0.x, u.d.ntok = x0.y, u.d.pos0 = x0.z, u.d.seq = x0.w;
-  u.d.kv0 = x1.x, u.d.kv1 = x1.y, u.d.slot = x1.z, u.d.row0 = x1.w;
+template <bool HOST, typename HU>
+__device__ __forceinline__ bool get_unit(const PrefillArgs& a, const HU& hu, int total, int r,
+                                         Unit& u) {
+  const unsigned c = (r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  const unsigned x = (unsigned)r * gridDim.x + c;
+  const unsigned i = x / (unsigned)a.G;
+  u.g = (int)(x - i * (unsigned)a.G);
+  if constexpr (HOST) {
+    if (x >= (unsigned)total) return false;
+    u.d = hu.u[i];
+  } else {
+    // read beside the number of units, not after it
+    const int4* p = reinterpret_cast<const int4*>(a.units + min(i, (unsigned)a.max_units - 1));
+    const int4 x0 = __ldcg(p), x1 = __ldcg(p + 1);
+    if (x >= (unsigned)total) return false;
+    u.d.tok0 = x0.x, u.d.ntok = x0.y, u.d.pos0 = x0.z, u.d.seq = x0.w;
+    u.d.kv0 = x1.x, u.d.kv1 = x1.y, u.d.slot = x1.z, u.d.row0 = x1.w;
+  }
   u.nt = u.d.kv1 - u.d.kv0;
+  u.dual = u.d.ntok <= a.TT;
+  if (u.dual) {
+    u.c0 = (u.nt + 1) / 2;
+    u.c1 = u.nt / 2;
+    return true;
+  }
   const int last0 = u.d.pos0 + min(u.d.ntok, a.TT) - 1;  // last position of row tile 0
   u.c0 = max(0, min(u.d.kv1, last0 / kKeys + 1) - u.d.kv0);
   u.c1 = u.d.ntok > a.TT ? u.nt : 0;
@@ -135,11 +170,12 @@ __device__ __forceinline__ const __nv_bfloat16* v_row(const PrefillArgs& a, cons
   return a.v + (int64_t)pg * a.page_stride + ((int64_t)(s % a.page_size) * a.G + u.g) * D;
 }
 
-template <int D>
+template <int D, bool HOST>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_k,
-                         const __grid_constant__ CUtensorMap map_v, const PrefillArgs a) {
+                         const __grid_constant__ CUtensorMap map_v, const PrefillArgs a,
+                         const __grid_constant__ std::conditional_t<HOST, HostUnits, NoHostUnits> hu) {
   using Cfg = PrefillCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -150,6 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t bar_full[Cfg::kSlots], bar_empty[Cfg::kSlots];
   __shared__ uint64_t bar_clean[2];  // V tiles cleaned, in turn
   __shared__ uint64_t bar_s_full[2], bar_p_most[2], bar_p_full[2], bar_pv_done[2], bar_drain;
+  __shared__ uint64_t bar_half_done, bar_half_read;  // dual units: tile 1's result, and its reading
+  __shared__ float half_m[kRows], half_l[kRows];
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
   __shared__ int odd_v[kFlagSlots];  // an infinity or NaN was taken out of the unit's V
@@ -160,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_q_full[i], 1);
       mbar_init(&bar_q_empty[i], 1);
-      mbar_init(&bar_clean[i], kCleanThreads);
+      mbar_init(&bar_clean[i], 128);
       mbar_init(&bar_s_full[i], 1);
       mbar_init(&bar_p_most[i], 128);
       mbar_init(&bar_p_full[i], 128);
@@ -171,8 +209,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar_empty[i], 1);
     }
     mbar_init(&bar_drain, 1);
+    mbar_init(&bar_half_done, 128);
+    mbar_init(&bar_half_read, 128);
     for (int i = 0; i < kFlagSlots; ++i) odd_v[i] = 0;
     fence_mbar_init();
+    // nothing else clears it without a plan, and no wait runs out before this
+    if (HOST && blockIdx.x == 0 && a.clear_err) *a.err = 0;
+  }
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&map_q);
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
   }
   if (warp == 0) {
     tmem_alloc(&tmem_base_s, 512);
@@ -183,18 +230,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
   volatile int* abort_flag = &abort_s;
-  const int total = __ldg(a.n_units) * a.G;
+  pdl_launch_dependents();
+  int total;
+  if constexpr (HOST) {
+    total = hu.n * a.G;
+  } else {
+    pdl_wait();  // for the units
+    total = __ldcg(a.n_units) * a.G;
+  }
   const int rounds = n_rounds(total);
 
   if (warp >= 8) {
     regs_decrease<kRegOther>();
     if (warp == kLoadWarp) {
       // ---------------- TMA loads ----------------
-      if (lane == 0) {
-        tma_prefetch_desc(&map_q);
-        tma_prefetch_desc(&map_k);
-        tma_prefetch_desc(&map_v);
-      }
       Ring<Cfg::kSlots> ring;
       uint32_t loads = 0;         // copies into the ring so far
       uint32_t qn[2] = {0, 0};    // Q tiles loaded so far
@@ -210,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < Cfg::kChunks; ++c)
               tma_load_4d(sQ + i * Cfg::kTileBytes + c * kRows * 128, &map_q, &bar_q_full[i], 0,
-                          u.g * a.HG, c, u.d.tok0 + i * a.TT);
+                          u.g * a.HG, c, u.d.tok0 + (u.dual ? 0 : i * a.TT));
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -239,25 +288,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int r = 0; r < rounds && ok; ++r) {
         Unit u;
-        if (!get_unit(a, total, r, u)) continue;
+        if (!get_unit<HOST>(a, hu, total, r, u)) continue;
         const int keys_end = u.d.pos0 + u.d.ntok;
+        // lane i: page of box i of a key tile (0: none, or packed rows)
+        auto page_of = [&](int j) {
+          const int key = (u.d.kv0 + j) * kKeys + lane * box_rows;
+          if (a.page_size == 0 || lane >= boxes || key >= keys_end || j >= u.nt) return 0;
+          return __ldg(a.block_table + (int64_t)u.d.seq * a.table_stride + key / a.page_size);
+        };
+        int page_next = page_of(0);
         for (int j = 0; j < u.nt && ok; ++j) {
           const int key0 = (u.d.kv0 + j) * kKeys;
-          int32_t row, page = 0;
+          int page = page_next;
+          page_next = page_of(j + 1);  // its latency behind this tile's waits
+          int32_t row = u.d.row0 + key0;
           int nbox = 1;
-          if (a.page_size == 0) {
-            row = u.d.row0 + key0;
-          } else {
+          if (a.page_size != 0) {
             const int left = (keys_end - key0 + box_rows - 1) / box_rows;
             nbox = left < boxes ? left : boxes;
-            const int key = key0 + lane * box_rows;
-            row = key % a.page_size;
-            if (lane < nbox) {
-              page = __ldg(a.block_table + (int64_t)u.d.seq * a.table_stride + key / a.page_size);
-              if (page < 0 || page >= a.num_pages) {
-                record_error(a.err, kDevBadIndex);
-                page = a.num_pages;  // outside the tensor: reads zeros
-              }
+            row = (key0 + lane * box_rows) % a.page_size;
+            if (lane < nbox && (page < 0 || page >= a.num_pages)) {
+              record_error(a.err, kDevBadIndex);
+              page = a.num_pages;  // outside the tensor: reads zeros
             }
           }
           if (j == 0) load_q(u, 0);
@@ -286,11 +338,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t k_desc = smem_desc_sw128(smem_u32(sR), 16, 1024);
       const uint64_t v_desc = smem_desc_sw128(smem_u32(sR), kKeys * 128, 1024);
       uint32_t qn[2] = {0, 0}, pn[2] = {0, 0}, cleaned = 0;
-      Ring<Cfg::kSlots> ring;
+      uint32_t base = 0;  // ring position of the unit's first tile: K_j at base + 2j, V_j after it
       bool ok = true;
-      auto issue_s = [&](int i, uint32_t slot, bool last) {
+      auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err, code));
+        return ok;
+      };
+      auto slot_of = [&](uint32_t x) { return x % Cfg::kSlots; };
+      auto wait_full = [&](uint32_t x) {
+        return wait(&bar_full[slot_of(x)], (x / Cfg::kSlots) & 1, kDevTimeoutLoad);
+      };
+      auto free_slot = [&](uint32_t x) {
+        if (elect_one()) umma_commit(&bar_empty[slot_of(x)]);
+        __syncwarp();
+      };
+      auto issue_s = [&](int i, uint32_t x, bool last) {
+        tc_fence_after();
         if (elect_one()) {
-          const uint64_t qd = q_desc + (uint32_t)i * kTile16, kd = k_desc + slot * kTile16;
+          const uint64_t qd = q_desc + (uint32_t)i * kTile16, kd = k_desc + slot_of(x) * kTile16;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * kRows * 128 + (kk & 3) * 32) / 16;
@@ -301,81 +366,104 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err, code));
-        return ok;
+      // O_i += P_i V once P_i is there
+      auto issue_pv = [&](int i, uint32_t x, bool first) {
+        const uint64_t vd = v_desc + slot_of(x) * kTile16;
+        auto step = [&](int kk) {  // keys 16kk .. 16kk+15
+          umma_f16_ts(tmem + kColO + i * 128, tmem + kColS + i * 128 + kk * 8,
+                      vd + (uint32_t)(kk * 16 * 128 / 16), idesc_o, (!first || kk > 0) ? 1u : 0u);
+        };
+        if (Cfg::kSplitP) {
+          if (!wait(&bar_p_most[i], pn[i] & 1, kDevTimeoutConsumer)) return;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 6; ++kk) step(kk);
+          }
+          __syncwarp();
+        }
+        if (!wait(&bar_p_full[i], pn[i] & 1, kDevTimeoutConsumer)) return;
+        ++pn[i];
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = Cfg::kSplitP ? 6 : 0; kk < 8; ++kk) step(kk);
+          umma_commit(&bar_pv_done[i]);
+        }
+        __syncwarp();
+      };
+      // V_j as loaded, or cleaned where some row does not see the whole tile
+      auto wait_v = [&](uint32_t x, bool clean) {
+        if (!clean) return wait_full(x);
+        const uint32_t c = cleaned++;
+        return wait(&bar_clean[c & 1], (c >> 1) & 1, kDevTimeoutConsumer);
       };
       for (int r = 0; r < rounds && ok; ++r) {
         Unit u;
-        if (!get_unit(a, total, r, u)) continue;
+        if (!get_unit<HOST>(a, hu, total, r, u)) continue;
         // broadcasts: known to be the same in every lane
         const int nt = __shfl_sync(0xffffffffu, u.nt, 0);
         const int cnt[2] = {__shfl_sync(0xffffffffu, u.c0, 0), __shfl_sync(0xffffffffu, u.c1, 0)};
         const int part0 = __shfl_sync(0xffffffffu, first_partial(u) - u.d.kv0, 0);
-        if (!wait(&bar_full[ring.slot], ring.phase, kDevTimeoutLoad)) break;
-        uint32_t k_slot = ring.slot;
-        ring.next();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (cnt[i] == 0) continue;
-          if (!wait(&bar_q_full[i], qn[i] & 1, kDevTimeoutLoad)) break;
-          ++qn[i];
-          tc_fence_after();
-          issue_s(i, k_slot, cnt[i] == 1);
-        }
-        if (!ok) break;
-        if (elect_one()) umma_commit(&bar_empty[k_slot]);
-        __syncwarp();
-        for (int j = 0; j < nt; ++j) {
-          const uint32_t v_slot = ring.slot;
-          // V as loaded, or cleaned where some row does not see the whole tile
-          if (j >= part0) {
-            if (!wait(&bar_clean[cleaned & 1], (cleaned >> 1) & 1, kDevTimeoutConsumer)) break;
-            ++cleaned;
-          } else {
-            if (!wait(&bar_full[v_slot], ring.phase, kDevTimeoutLoad)) break;
-          }
-          ring.next();
-          if (j + 1 < nt) {
-            if (!wait(&bar_full[ring.slot], ring.phase, kDevTimeoutLoad)) break;
-            k_slot = ring.slot;
-            ring.next();
-          }
+        const bool dual = __shfl_sync(0xffffffffu, (int)u.dual, 0) != 0;
+        if (dual) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if (j >= cnt[i]) continue;
-            const uint64_t vd = v_desc + v_slot * kTile16;
-            auto issue_pv = [&](int kk) {  // keys 16kk .. 16kk+15
-              umma_f16_ts(tmem + kColO + i * 128, tmem + kColS + i * 128 + kk * 8,
-                          vd + (uint32_t)(kk * 16 * 128 / 16), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-            };
-            if (Cfg::kSplitP) {
-              if (!wait(&bar_p_most[i], pn[i] & 1, kDevTimeoutConsumer)) break;
-              tc_fence_after();
-              if (elect_one()) {
+            if (cnt[i] == 0) continue;
+            if (!wait_full(base + 2 * i)) break;
+            if (!wait(&bar_q_full[i], qn[i] & 1, kDevTimeoutLoad)) break;
+            ++qn[i];
+            issue_s(i, base + 2 * i, cnt[i] == 1);
+            free_slot(base + 2 * i);
+          }
+          for (int j = 0; j < nt && ok; j += 2) {
 #pragma unroll
-                for (int kk = 0; kk < 6; ++kk) issue_pv(kk);
+            for (int i = 0; i < 2; ++i) {
+              const int jj = j + i;
+              if (jj >= nt) continue;
+              const uint32_t x = base + 2 * jj;
+              if (!wait_v(x + 1, jj >= part0)) break;
+              issue_pv(i, x + 1, jj < 2);
+              if (!ok) break;
+              free_slot(x + 1);
+              if (jj + 2 < nt) {
+                if (!wait_full(x + 4)) break;
+                issue_s(i, x + 4, jj + 4 >= nt);
+                free_slot(x + 4);
               }
-              __syncwarp();
             }
-            if (!wait(&bar_p_full[i], pn[i] & 1, kDevTimeoutConsumer)) break;
-            ++pn[i];
-            tc_fence_after();
-            if (elect_one()) {
+          }
+        } else {
+          if (!wait_full(base)) break;
 #pragma unroll
-              for (int kk = Cfg::kSplitP ? 6 : 0; kk < 8; ++kk) issue_pv(kk);
-              umma_commit(&bar_pv_done[i]);
-            }
-            __syncwarp();
-            if (j + 1 < cnt[i]) issue_s(i, k_slot, j + 2 == cnt[i]);
+          for (int i = 0; i < 2; ++i) {
+            if (cnt[i] == 0) continue;
+            if (!wait(&bar_q_full[i], qn[i] & 1, kDevTimeoutLoad)) break;
+            ++qn[i];
+            issue_s(i, base, cnt[i] == 1);
           }
           if (!ok) break;
-          if (elect_one()) {
-            umma_commit(&bar_empty[v_slot]);
-            if (j + 1 < nt) umma_commit(&bar_empty[k_slot]);
+          free_slot(base);
+          for (int j = 0; j < nt; ++j) {
+            const uint32_t x = base + 2 * j;
+            if (!wait_v(x + 1, j >= part0)) break;
+            if (j + 1 < nt && !wait_full(x + 2)) break;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (j >= cnt[i]) continue;
+              issue_pv(i, x + 1, j == 0);
+              if (!ok) break;
+              if (j + 1 < cnt[i]) issue_s(i, x + 2, j + 2 == cnt[i]);
+            }
+            if (!ok) break;
+            if (elect_one()) {
+              umma_commit(&bar_empty[slot_of(x + 1)]);
+              if (j + 1 < nt) umma_commit(&bar_empty[slot_of(x + 2)]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
+        base += 2 * nt;
       }
       // after an abort every product issued must be done before TMEM and shared
       // memory go; the drain barrier is used for nothing else
@@ -383,61 +471,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         volatile int no_abort = 0;
         umma_commit(&bar_drain);
         mbar_wait(&bar_drain, 0, &no_abort, nullptr, 0);
-      }
-    } else {
-      // ---------------- cleaning of V ----------------
-      const int x = (int)threadIdx.x - kCleanWarp0 * 32;
-      Ring<Cfg::kSlots> ring;
-      int n = 0;
-      uint32_t cleaned = 0;
-      bool ok = true;
-      for (int r = 0; r < rounds && ok; ++r) {
-        Unit u;
-        if (!get_unit(a, total, r, u)) continue;
-        const int part0 = first_partial(u) - u.d.kv0;
-        const int keys_end = u.d.pos0 + u.d.ntok;
-        if (x == 0) odd_v[n % kFlagSlots] = 0;
-        for (int j = 0; j < u.nt && ok; ++j) {
-          ring.next();  // past the K tile
-          const uint32_t slot = ring.slot;
-          ok = mbar_wait(&bar_full[slot], ring.phase, abort_flag, a.err, kDevTimeoutLoad);
-          ring.next();
-          if (!ok || j < part0) continue;
-          const int key0 = (u.d.kv0 + j) * kKeys;
-          uint8_t* base = sR + slot * Cfg::kTileBytes;
-          bool odd = false;
-          // 16-byte pieces, 8 per 128-byte line, lines chunk-major; where a
-          // piece lies within its line does not matter
-          for (int p = x; p < Cfg::kTileBytes / 16; p += kCleanThreads) {
-            const int line = p >> 3;
-            const int key = key0 + (line & (kKeys - 1));
-            if (key <= u.d.pos0) continue;  // every row sees it
-            uint4* w = reinterpret_cast<uint4*>(base) + p;
-            if (key >= keys_end) {
-              *w = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 v = *w;
-            uint32_t* e = &v.x;
-            bool bad = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              bad |= (((e[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u) != 0;
-            if (bad) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if ((e[i] & 0x7F80u) == 0x7F80u) e[i] &= 0xFFFF0000u;
-                if ((e[i] & 0x7F800000u) == 0x7F800000u) e[i] &= 0x0000FFFFu;
-              }
-              *w = v;
-              odd = true;
-            }
-          }
-          if (odd) odd_v[n % kFlagSlots] = 1;
-          fence_async_smem();
-          mbar_arrive(&bar_clean[cleaned++ & 1]);
-        }
-        ++n;
       }
     }
   } else {
@@ -451,20 +484,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = lane_addr + kColS + i * 128;
     const uint32_t o_addr = lane_addr + kColO + i * 128;
     const uint64_t k2 = f2_pack(a.scale_log2, a.scale_log2);
-    uint32_t sn = 0, pvn = 0;
+    uint32_t sn = 0, pvn = 0, halves = 0;
     int n = 0;
+    uint32_t base = 0;  // ring position of the unit's first tile
+    uint32_t cleaned = 0;  // V tiles cleaned in the units before
+    int prev_nt = 0, prev_special = 0;
     bool ok = true;
+    // Takes infinities and NaNs, and rows past the sequence's end, out of V tile
+    // j of a unit.
+    auto clean = [&](const Unit& u, int j, int flag_slot) {
+      const uint32_t x = base + 2 * j + 1;
+      const uint32_t slot = x % Cfg::kSlots;
+      if (!mbar_wait(&bar_full[slot], (x / Cfg::kSlots) & 1, abort_flag, a.err, kDevTimeoutLoad))
+        return false;
+      const int key0 = (u.d.kv0 + j) * kKeys, keys_end = u.d.pos0 + u.d.ntok;
+      // 16-byte pieces, 8 per 128-byte line, lines chunk-major; where a piece
+      // lies within its line does not matter
+      uint4* tile = reinterpret_cast<uint4*>(sR + slot * Cfg::kTileBytes);
+      bool odd = false;
+#pragma unroll 4
+      for (int q = (int)threadIdx.x & 127; q < Cfg::kTileBytes / 16; q += 128) {
+        uint4 v = tile[q];
+        uint32_t* e = &v.x;
+        uint32_t bad = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) bad |= ((e[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+        const int key = key0 + ((q >> 3) & (kKeys - 1));
+        if (key >= keys_end) {
+          tile[q] = make_uint4(0, 0, 0, 0);
+        } else if (bad != 0 && key > u.d.pos0) {  // some row does not see it
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if ((e[k] & 0x7F80u) == 0x7F80u) e[k] &= 0xFFFF0000u;
+            if ((e[k] & 0x7F800000u) == 0x7F800000u) e[k] &= 0x0000FFFFu;
+          }
+          tile[q] = v;
+          odd = true;
+        }
+      }
+      if (odd) odd_v[flag_slot] = 1;
+      fence_async_smem();
+      return true;
+    };
     for (int r = 0; r < rounds && ok; ++r) {
       Unit u;
-      if (!get_unit(a, total, r, u)) continue;
-      const int flag_slot = n++ % kFlagSlots;
+      if (!get_unit<HOST>(a, hu, total, r, u)) continue;
+      base += 2 * prev_nt;
+      cleaned += prev_special;
+      const int part0 = first_partial(u) - u.d.kv0;
+      prev_nt = u.nt;
+      prev_special = max(0, u.nt - max(part0, 0));
+      const int flag_slot = n % kFlagSlots;
+      // of the unit after next: nobody sets or reads it any more or yet
+      if (threadIdx.x == 0) odd_v[(n + 2) % kFlagSlots] = 0;
+      ++n;
       const int cnt = i == 0 ? u.c0 : u.c1;
-      const int tok = i * a.TT + tt;  // token of this row within the unit
+      const int tok = (u.dual ? 0 : i * a.TT) + tt;  // token of this row within the unit
       const bool valid = tt < a.TT && tok < u.d.ntok;
       const int pos = u.d.pos0 + tok;
       float m = -INFINITY, l = 0.f;  // m: of the raw scores
       for (int j = 0; j < cnt; ++j) {
-        const int lim = valid ? pos - (u.d.kv0 + j) * kKeys : kKeys;
+        const int jt = u.dual ? 2 * j + i : j;  // key tile of the unit, and of the sequence
+        const int kt = u.d.kv0 + jt;
+        // While S is on its way: clean V, where some row does not see all of it.
+        // One warpgroup does, the first that takes the tile.
+        if (jt >= part0 && (i == 0 || u.dual || jt >= u.c0)) {
+          ok = clean(u, jt, flag_slot);
+          if (!ok) break;
+          mbar_arrive(&bar_clean[(cleaned + jt - max(part0, 0)) & 1]);
+        }
+        const int lim = valid ? pos - kt * kKeys : kKeys;
         ok = mbar_wait(&bar_s_full[i], sn & 1, abort_flag, a.err, kDevTimeoutMma);
         if (!ok) break;
         ++sn;
@@ -558,78 +647,111 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
       }
-      const bool odd = cnt > 0 && *reinterpret_cast<volatile int*>(&odd_v[flag_slot]) != 0;
-      const int64_t slot = u.d.slot >= 0 ? (int64_t)u.d.slot + u.g : -1;
-      const int prow = i * kRows + row;  // row of the unit
-      if (slot >= 0) {
-        // one part of a split unit: O unnormalised, with its maximum (log2 domain) and sum
-        float* dst = a.part_o + (slot * 2 * kRows + prow) * D;
-        const int k_lo = max(u.d.pos0 + 1, u.d.kv0 * kKeys);
-        const int k_hi = min(pos, u.d.kv1 * kKeys - 1);
+      if (u.dual) {
+        if (i == 1) {
+          // hand the maximum and sum to the other warpgroup's thread of this row,
+          // which reads O from TMEM itself
+          half_m[row] = m;
+          half_l[row] = l;
+          tc_fence_before();
+          mbar_arrive(&bar_half_done);
+          ok = mbar_wait(&bar_half_read, halves & 1, abort_flag, a.err, kDevTimeoutConsumer);
+          ++halves;
+          if (!ok) break;
+          continue;
+        }
+        ok = mbar_wait(&bar_half_done, halves & 1, abort_flag, a.err, kDevTimeoutConsumer);
+        ++halves;
+        if (!ok) break;
+        tc_fence_after();
+        const float m1 = half_m[row], l1 = half_l[row];
+        const float mn = fmaxf(m, m1), mu = mn > -INFINITY ? mn : 0.f;
+        const float w0 = fast_exp2((m - mu) * a.scale_log2);
+        const float w1 = fast_exp2((m1 - mu) * a.scale_log2);
+        m = mn;
+        l = l * w0 + l1 * w1;
+        if (u.c1 > 0) {  // O_0 = w0 O_0 + w1 O_1, in place
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          uint32_t o[16];
-          if (cnt > 0) {
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16], o2[16];
             tmem_ld_32x32b_x16(o_addr + c, o);
+            tmem_ld_32x32b_x16(o_addr + 128 + c, o2);
             tmem_wait();
             reg_fence(o);
-          } else {
+            reg_fence(o2);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0;
+            for (int e = 0; e < 16; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * w0 + __uint_as_float(o2[e]) * w1);
+            tmem_st_32x32b_x16(o_addr + c, o);
           }
-          if (odd && valid) {
-            for (int s = k_lo; s <= k_hi; ++s) {
-              const __nv_bfloat16* vr = v_row(a, u, s, D);
-              if (!vr) continue;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float v = __bfloat162float(vr[c + e]);
-                if (!(fabsf(v) <= 3.4e38f)) o[e] = __float_as_uint(__uint_as_float(o[e]) + v);
-              }
-            }
-          }
-          if (valid) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          }
+          tmem_wait_st();
         }
-        if (valid) a.part_ml[slot * 2 * kRows + prow] = make_float2(m * a.scale_log2, l);
-        tc_fence_before();
-        continue;
       }
-      const float inv = 1.f / l;
-      __nv_bfloat16* dst =
-          a.out + (((int64_t)u.d.tok0 + tok) * a.H + u.g * a.HG + (row - tt * a.HG)) * D;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      // 32 columns of O
+      auto load_o = [&](int c, float (&f)[32]) {
         uint32_t o[32];
         tmem_ld_32x32b_x32(o_addr + c, o);
         tmem_wait();
         reg_fence(o);
-        if (!valid) continue;
-        float f[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * inv;
-        if (odd) {
-          for (int s = u.d.pos0 + 1; s <= pos; ++s) {
-            const __nv_bfloat16* vr = v_row(a, u, s, D);
-            if (!vr) continue;
+        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]);
+      };
+      const bool odd = *reinterpret_cast<volatile int*>(&odd_v[flag_slot]) != 0;
+      // infinities and NaNs taken out of V, back into the rows that see their keys
+      auto add_odd = [&](int c, float (&f)[32]) {
+        const int lo = max(u.d.pos0 + 1, u.d.kv0 * kKeys);
+        const int hi = min(pos, u.d.kv1 * kKeys - 1);
+        for (int s = lo; s <= hi; ++s) {
+          const __nv_bfloat16* vr = v_row(a, u, s, D);
+          if (!vr) continue;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float v = __bfloat162float(vr[c + e]);
-              if (!(fabsf(v) <= 3.4e38f)) f[e] += v;
-            }
+          for (int e = 0; e < 32; ++e) {
+            const float v = __bfloat162float(vr[c + e]);
+            if (!(fabsf(v) <= 3.4e38f)) f[e] += v;
           }
         }
-        uint32_t w[16];
+      };
+      if (u.d.slot >= 0) {
+        // one part of a split unit: O unnormalised, with its maximum (log2 domain) and sum
+        const int64_t prow = ((int64_t)u.d.slot + u.g) * 2 * kRows + i * kRows + row;
+        float* dst = a.part_o + prow * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float f[32];
+          if (cnt > 0) {
+            load_o(c, f);
+          } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
-        // a row's 32-byte sectors whole: no staging for coalesced stores
-        st_global_32(dst + c, w);
-        st_global_32(dst + c + 16, w + 8);
+            for (int e = 0; e < 32; ++e) f[e] = 0.f;
+          }
+          if (!valid) continue;
+          if (odd) add_odd(c, f);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            st_global_32(dst + c + e, reinterpret_cast<const uint32_t*>(f + e));
+        }
+        if (valid) a.part_ml[prow] = make_float2(m * a.scale_log2, l);
+      } else if (cnt > 0) {
+        const float inv = 1.f / l;
+        __nv_bfloat16* dst =
+            a.out + (((int64_t)u.d.tok0 + tok) * a.H + u.g * a.HG + (row - tt * a.HG)) * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float f[32];
+          load_o(c, f);
+          if (!valid) continue;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) f[e] *= inv;
+          if (odd) add_odd(c, f);
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+          st_global_32(dst + c, w);  // whole sectors: no staging for coalesced stores
+          st_global_32(dst + c + 16, w + 8);
+        }
       }
       tc_fence_before();
+      if (u.dual) mbar_arrive(&bar_half_read);
     }
   }
 
@@ -639,13 +761,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// The units of a batch, longest first.  One CTA: counts the units and their key
-// tiles, decides whether units are split along the keys, and places every unit
-// (or part) by a counting sort over its number of key tiles (buckets of an
-// eighth of an octave).
+// The units of a batch.  One CTA: counts the units and their key tiles and decides
+// whether they are split along the keys.  Units that fit the GPU at once are split
+// so that their parts still do, into the shortest parts that allows; the rest are
+// placed longest first, by a counting sort over their number of key tiles (buckets
+// of an eighth of an octave), and split where one alone would outlast an even share.
+// Clears the call's error word.
 // ---------------------------------------------------------------------------
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;  // at most
 constexpr int kBuckets = 256;
+constexpr int kMinPart = 4;  // key tiles worth a part: its overhead is about three
 
 __device__ __forceinline__ int bucket_of(int tiles) {  // longer first; tiles >= 1
   const int e = 31 - __clz(tiles);
@@ -657,8 +782,9 @@ struct PlanArgs {
   const int64_t* cu;          // device offsets of the new tokens, or null: `off`
   const int32_t* seq_lens;    // device, null: whole prompts
   int32_t B, T, G, TT, table_rows;  // table_rows: keys a row of the block table holds
-  int32_t split_ctas;         // CTAs to keep busy; 0: never split
-  int32_t max_slots, max_units;
+  int32_t ctas;               // CTAs to keep busy
+  int32_t can_split;          // room for partial results
+  int32_t max_units, clear_err;
   DenseUnit* units;
   DenseSplit* splits;
   int32_t* counts;            // [0] units, [1] split units
@@ -670,6 +796,7 @@ __device__ __forceinline__ void plan_seq(const PlanArgs& p, const DenseOffsets& 
                                          int64_t& a, int& n, int& pos) {
   const int64_t lo = p.cu ? __ldg(p.cu + b) : off.cu[b];
   const int64_t hi = p.cu ? __ldg(p.cu + b + 1) : off.cu[b + 1];
+  const int L = p.seq_lens ? __ldg(p.seq_lens + b) : 0;
   a = lo;
   n = 0;
   pos = 0;
@@ -678,7 +805,6 @@ __device__ __forceinline__ void plan_seq(const PlanArgs& p, const DenseOffsets& 
     return;
   }
   if (p.seq_lens && hi > lo) {
-    const int L = __ldg(p.seq_lens + b);
     if (L < hi - lo || L > p.table_rows) {
       record_error(p.err, kDevBadIndex);
       return;
@@ -688,165 +814,218 @@ __device__ __forceinline__ void plan_seq(const PlanArgs& p, const DenseOffsets& 
   n = (int)(hi - lo);
 }
 
-__device__ __forceinline__ unsigned long long block_sum64(unsigned long long v,
-                                                          unsigned long long* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (lane_id() == 0) red[warp_id()] = v;
-  __syncthreads();
-  unsigned long long s = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) s += red[w];
-  __syncthreads();
-  return s;
-}
-
 __global__ void __launch_bounds__(kPlanThreads)
     dense_plan_kernel(const __grid_constant__ DenseOffsets off, const PlanArgs p) {
   __shared__ int hist[kBuckets];
-  __shared__ unsigned long long red[kPlanThreads / 32];
-  __shared__ int longest_s, n_split_s, n_slot_s;
-  const int tid = threadIdx.x;
-  if (tid == 0) longest_s = 0, n_split_s = 0, n_slot_s = 0;
-  for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
+  __shared__ unsigned long long sum_s;
+  __shared__ int longest_s, n_units_s, n_split_s, n_slot_s, part_s;
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, warps = blockDim.x / 32;
+  if (tid == 0) {
+    if (p.clear_err) *p.err = 0;
+    sum_s = 0, longest_s = 0, n_units_s = 0, n_split_s = 0, n_slot_s = 0, part_s = 1 << 30;
+  }
+  for (int i = tid; i < kBuckets; i += blockDim.x) hist[i] = 0;
   __syncthreads();
   const int U = 2 * p.TT;  // tokens per unit
-  // ---- how much work there is ----
-  // A warp per sequence, a lane per unit of it.
-  unsigned long long tiles = 0;
-  int longest = 0;
-  for (int b = warp_id(); b < p.B; b += kPlanThreads / 32) {
-    int64_t a;
-    int n, pos;
-    plan_seq(p, off, b, a, n, pos);
-    for (int i = lane_id() * U; i < n; i += 32 * U) {
-      const int nt = (pos + min(n, i + U) - 1) / kKeys + 1;
-      tiles += nt;
-      longest = max(longest, nt);
-    }
-  }
-  atomicMax(&longest_s, longest);
-  const unsigned long long sum = block_sum64(tiles, red) * p.G;
-  // ---- split the longest units when they would outlast an even share ----
-  int part = 1 << 30;
-  if (p.split_ctas > 0) {
-    const int share = (int)((sum + p.split_ctas - 1) / p.split_ctas);
-    if (longest_s > share + share / 4) part = max(share, 4);
-  }
+  // a warp per sequence, a lane per unit of it
   auto for_units = [&](auto&& f) {
-    for (int b = warp_id(); b < p.B; b += kPlanThreads / 32) {
+    for (int b = warp_id(); b < p.B; b += warps) {
       int64_t a;
       int n, pos;
       plan_seq(p, off, b, a, n, pos);
-      for (int i = lane_id() * U; i < n; i += 32 * U) {
-        const int nt = (pos + min(n, i + U) - 1) / kKeys + 1;
-        const int parts = (nt + part - 1) / part;
-        f(b, a, i, n, pos, nt, parts);
-      }
+      for (int i = lane_id() * U; i < n; i += 32 * U)
+        f(b, a, i, min(U, n - i), pos + i, (pos + min(n, i + U) - 1) / kKeys + 1);
     }
   };
-  for_units([&](int, int64_t, int, int, int, int nt, int parts) {
-    const int len = (nt + parts - 1) / parts;
-    for (int k = 0; k < parts; ++k) {
-      const int c = min(len, nt - k * len);
-      if (c > 0) atomicAdd(&hist[bucket_of(c)], 1);
-    }
-  });
-  __syncthreads();
-  if (tid < 32) {  // exclusive prefix over the buckets
-    int run = 0;
-    for (int i = 0; i < kBuckets; i += 32) {
-      int v = hist[i + tid], x = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (tid >= o) x += y;
-      }
-      hist[i + tid] = run + x - v;
-      run += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (tid == 0) p.counts[0] = min(run, p.max_units);
+  // ---- how much work there is ----
+  {
+    unsigned long long tiles = 0;
+    int longest = 0, n = 0;
+    for_units([&](int, int64_t, int, int ntok, int, int nt) {
+      const int w = ntok <= p.TT ? (nt + 1) / 2 : nt;  // see weight below
+      tiles += w;
+      longest = max(longest, w);
+      ++n;
+    });
+    atomicAdd(&sum_s, tiles);
+    atomicMax(&longest_s, longest);
+    atomicAdd(&n_units_s, n);
   }
   __syncthreads();
-  for_units([&](int b, int64_t a, int i, int n, int pos, int nt, int parts) {
-    const int len = (nt + parts - 1) / parts;
-    parts = (nt + len - 1) / len;
-    DenseUnit d;
-    d.tok0 = (int)a + i;
-    d.ntok = min(U, n - i);
-    d.pos0 = pos + i;
-    d.seq = b;
-    d.slot = -1;
-    d.row0 = p.seq_lens ? 0 : (int)a;
+  const bool one_wave = (long long)n_units_s * p.G <= p.ctas;
+  const int share = (int)((sum_s * p.G + p.ctas - 1) / p.ctas);
+  // a unit of one row tile is taken by both softmax warpgroups: half as long
+  auto weight = [&](int ntok, int nt) { return ntok <= p.TT ? (nt + 1) / 2 : nt; };
+  int part = 1 << 30;  // longest part, by weight
+  if (!p.can_split) {
+  } else if (one_wave) {
+    // the shortest parts that leave at most one per CTA: a warp per candidate
+    for (int base = max(kMinPart, share); base < longest_s; base += warps) {
+      const int c = base + (int)warp_id();
+      long long n = 0;
+      for (int b = 0; b < p.B; ++b) {
+        int64_t a;
+        int len, pos;
+        plan_seq(p, off, b, a, len, pos);
+        for (int i = (int)lane_id() * U; i < len; i += 32 * U) {
+          const int w = weight(min(U, len - i), (pos + min(len, i + U) - 1) / kKeys + 1);
+          n += (w + c - 1) / c;
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      if (lane_id() == 0 && n * p.G <= p.ctas) atomicMin(&part_s, c);
+      __syncthreads();
+      const int found = part_s;
+      __syncthreads();
+      if (found < 1 << 30) break;
+    }
+    part = part_s;
+  } else if (longest_s > share + share / 4) {
+    part = max(share, kMinPart);
+  }
+  // parts of a unit, and the key tiles of each
+  auto parts_of = [&](int ntok, int nt, int& len) {
+    const int w = weight(ntok, nt);
+    const int k = w > part ? (w + part - 1) / part : 1;
+    len = (nt + k - 1) / k;
+    return (nt + len - 1) / len;
+  };
+  if (!one_wave) {
+    for_units([&](int, int64_t, int, int ntok, int, int nt) {
+      int len;
+      const int parts = parts_of(ntok, nt, len);
+      for (int k = 0; k < parts; ++k) atomicAdd(&hist[bucket_of(min(len, nt - k * len))], 1);
+    });
+    __syncthreads();
+    if (tid < 32) {  // exclusive prefix over the buckets
+      int run = 0;
+      for (int i = 0; i < kBuckets; i += 32) {
+        const int v = hist[i + tid];
+        int x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (tid >= o) x += y;
+        }
+        hist[i + tid] = run + x - v;
+        run += __shfl_sync(0xffffffffu, x, 31);
+      }
+      if (tid == 0) n_units_s = run;
+    }
+    __syncthreads();
+  }
+  for_units([&](int b, int64_t a, int i, int ntok, int pos0, int nt) {
+    int len;
+    const int parts = parts_of(ntok, nt, len);
     int slot = -1;
     if (parts > 1) {
       slot = atomicAdd(&n_slot_s, parts * p.G);
       const int x = atomicAdd(&n_split_s, 1);
-      DenseSplit sp;
-      sp.tok0 = d.tok0, sp.ntok = d.ntok, sp.slot = slot, sp.parts = parts;
-      p.splits[x] = sp;
+      *reinterpret_cast<int4*>(p.splits + x) = make_int4((int)a + i, ntok, slot, parts);
     }
     for (int k = 0; k < parts; ++k) {
-      d.kv0 = k * len;
-      d.kv1 = min(nt, (k + 1) * len);
-      d.slot = slot < 0 ? -1 : slot + k * p.G;
-      const int x = atomicAdd(&hist[bucket_of(d.kv1 - d.kv0)], 1);
+      const int kv1 = min(nt, (k + 1) * len);
+      const int x = one_wave ? atomicAdd(&hist[0], 1) : atomicAdd(&hist[bucket_of(kv1 - k * len)], 1);
       if (x < p.max_units) {
         int4* dst = reinterpret_cast<int4*>(p.units + x);
-        dst[0] = make_int4(d.tok0, d.ntok, d.pos0, d.seq);
-        dst[1] = make_int4(d.kv0, d.kv1, d.slot, d.row0);
+        dst[0] = make_int4((int)a + i, ntok, pos0, b);
+        dst[1] = make_int4(k * len, kv1, slot < 0 ? -1 : slot + k * p.G,
+                           p.seq_lens ? 0 : (int)a);
       }
     }
   });
   __syncthreads();
-  if (tid == 0) p.counts[1] = n_split_s;
+  if (tid == 0) {
+    p.counts[0] = min(one_wave ? hist[0] : n_units_s, p.max_units);
+    p.counts[1] = n_split_s;
+  }
 }
 
-// out = sum_z 2^(m_z - M) O_z / sum_z 2^(m_z - M) l_z over the parts z of every
+// out = sum_z 2^(m_z - M) O_z / sum_z 2^(m_z - M) l_z over the partials z of every
 // split unit; a warp per row, D/32 columns a lane.
-template <int D>
+template <int D, bool HOST>
 __global__ void __launch_bounds__(256)
-    dense_combine_kernel(const DenseSplit* splits, const int32_t* counts, const float* part_o,
+    dense_combine_kernel(const __grid_constant__ std::conditional_t<HOST, HostSplits, NoHostUnits> hs,
+                         const DenseSplit* splits, const int32_t* counts, const float* part_o,
                          const float2* part_ml, int H, int G, int TT, __nv_bfloat16* out) {
+  pdl_wait();
   const int HG = H / G;
-  const int n = __ldg(counts + 1);
-  const int64_t rows = (int64_t)n * G * 2 * kRows;
+  int n;
+  if constexpr (HOST)
+    n = hs.n;
+  else
+    n = __ldcg(counts + 1);
+  const int per_tile = TT * HG, per_unit = 2 * per_tile;  // rows
+  const unsigned rows = (unsigned)n * G * per_unit;       // at most (CTAs / 2) * 256
   const int lane = lane_id();
   constexpr int C = D / 32;
-  for (int64_t x = (int64_t)blockIdx.x * 8 + warp_id(); x < rows; x += (int64_t)gridDim.x * 8) {
-    const int prow = (int)(x % (2 * kRows));
-    const int64_t y = x / (2 * kRows);
+  for (unsigned x = blockIdx.x * 8 + warp_id(); x < rows; x += gridDim.x * 8) {
+    const unsigned y = x / per_unit;
+    const int urow = (int)(x - y * per_unit);
     const int g = (int)(y % G);
-    const int4 sp = __ldg(reinterpret_cast<const int4*>(splits + y / G));
-    const int tile = prow / kRows, row = prow % kRows;
-    const int tt = row / HG, tok = tile * TT + tt;
-    if (tt >= TT || tok >= sp.y) continue;
-    // lane z reads part z's maximum and sum
-    float M = -INFINITY;
-    for (int z = lane; z < sp.w; z += 32)
-      M = fmaxf(M, part_ml[((int64_t)sp.z + (int64_t)z * G + g) * 2 * kRows + prow].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (!(M > -INFINITY)) M = 0.f;
-    float L = 0.f, acc[C];
+    int4 sp;
+    if constexpr (HOST) {
+      const DenseSplit& d = hs.s[y / G];
+      sp = make_int4(d.tok0, d.ntok, d.slot, d.parts);
+    } else {
+      sp = __ldcg(reinterpret_cast<const int4*>(splits + y / G));
+    }
+    const int tok = urow / HG, hh = urow - tok * HG;
+    if (tok >= sp.y) continue;
+    const int prow = tok >= TT ? kRows + urow - per_tile : urow;  // row of the partial
+    const int np = sp.w;
+    auto at = [&](int z) {  // row of partial z
+      return ((int64_t)sp.z + (int64_t)z * G + g) * 2 * kRows + prow;
+    };
+    float M = -INFINITY, L = 0.f, acc[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = 0.f;
-#pragma unroll 4
-    for (int z = 0; z < sp.w; ++z) {
-      const int64_t pr = ((int64_t)sp.z + (int64_t)z * G + g) * 2 * kRows + prow;
-      const float2 ml = __ldg(part_ml + pr);
-      const float w = fast_exp2(ml.x - M);
-      L += w * ml.y;
-      const float* src = part_o + pr * D + lane * C;
-      if constexpr (C == 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(src));
-        acc[0] += w * v.x, acc[1] += w * v.y, acc[2] += w * v.z, acc[3] += w * v.w;
-      } else {
-        const float2 v = __ldg(reinterpret_cast<const float2*>(src));
-        acc[0] += w * v.x, acc[1] += w * v.y;
+    for (int z0 = 0; z0 < np; z0 += 32) {
+      // lane z: partial z's maximum and sum
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (z0 + lane < np) ml = __ldcg(part_ml + at(z0 + lane));
+      float mx = ml.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float mn = fmaxf(M, mx), mu = mn > -INFINITY ? mn : 0.f;
+      const float f0 = fast_exp2(M - mu);
+      const float w = fast_exp2(ml.x - mu);
+      float ls = w * ml.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+      L = L * f0 + ls;
+      M = mn;
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] *= f0;
+      const int m = min(32, np - z0);
+      // 8 rows' loads in flight at a time
+      for (int z1 = 0; z1 < m; z1 += 8) {
+        float v[8][C];
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          const float* src = part_o + at(z0 + min(z1 + z, m - 1)) * D + lane * C;
+          if constexpr (C == 4) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
+            v[z][0] = y.x, v[z][1] = y.y, v[z][2] = y.z, v[z][3] = y.w;
+          } else {
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
+            v[z][0] = y.x, v[z][1] = y.y;
+          }
+        }
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          const float f = __shfl_sync(0xffffffffu, w, z1 + z);
+          if (z1 + z < m) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) acc[c] += f * v[z][c];
+          }
+        }
       }
     }
     const float inv = 1.f / L;
-    __nv_bfloat16* o = out + (((int64_t)sp.x + tok) * H + g * HG + (row - tt * HG)) * D + lane * C;
+    __nv_bfloat16* o = out + (((int64_t)sp.x + tok) * H + g * HG + hh) * D + lane * C;
     if constexpr (C == 4) {
       *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
                                                 pack_bf16x2(acc[2] * inv, acc[3] * inv));
@@ -854,6 +1033,104 @@ __global__ void __launch_bounds__(256)
       *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
     }
   }
+}
+
+// A launch that may start while the kernel before it in the stream still runs
+// (the kernel calls pdl_wait before it touches what that one writes).
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kern)(Params...), int grid, int threads, int smem, cudaStream_t s,
+                         Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// The plan of a batch with host offsets, by the rules of dense_plan_kernel; false
+// when it has more units than travel as a parameter.
+bool host_plan(const DensePrefillLaunch& p, int TT, HostUnits& hu, HostSplits& hs) {
+  const int U = 2 * TT;
+  int n = 0, longest = 0;
+  int64_t sum = 0;
+  int w[kHostUnits];
+  auto tiles = [&](int len, int i) { return ((i + U < len ? i + U : len) - 1) / kKeys + 1; };
+  auto weight = [&](int len, int i) {
+    const int nt = tiles(len, i);
+    return len - i <= TT ? (nt + 1) / 2 : nt;
+  };
+  if (p.T / U > kHostUnits) return false;
+  for (int b = 0; b < p.B; ++b) {
+    const int len = (int)(p.offsets->cu[b + 1] - p.offsets->cu[b]);
+    for (int i = 0; i < len; i += U) {
+      if (n == kHostUnits) return false;
+      w[n] = weight(len, i);
+      sum += w[n];
+      longest = w[n] > longest ? w[n] : longest;
+      ++n;
+    }
+  }
+  const int ctas = p.grid;
+  const bool one_wave = (int64_t)n * p.G <= ctas;
+  const int share = (int)((sum * p.G + ctas - 1) / ctas);
+  int part = 1 << 30;
+  if (p.max_slots > 0) {
+    if (one_wave) {
+      for (int c = share > kMinPart ? share : kMinPart; c < longest; ++c) {
+        int64_t m = 0;
+        for (int i = 0; i < n; ++i) m += (w[i] + c - 1) / c;
+        if (m * p.G <= ctas) {
+          part = c;
+          break;
+        }
+      }
+    } else if (longest > share + share / 4) {
+      part = share > kMinPart ? share : kMinPart;
+    }
+  }
+  hu.n = hs.n = 0;
+  int slots = 0;
+  for (int b = 0; b < p.B; ++b) {
+    const int a = (int)p.offsets->cu[b], len = (int)p.offsets->cu[b + 1] - a;
+    for (int i = 0; i < len; i += U) {
+      const int nt = tiles(len, i), wt = weight(len, i);
+      int k = wt > part ? (wt + part - 1) / part : 1;
+      const int plen = (nt + k - 1) / k;
+      k = (nt + plen - 1) / plen;
+      const int ntok = len - i < U ? len - i : U;
+      if (hu.n + k > kHostUnits || (k > 1 && hs.n == kHostUnits / 2)) return false;
+      if (k > 1) hs.s[hs.n++] = DenseSplit{a + i, ntok, slots, k};
+      for (int x = 0; x < k; ++x) {
+        const int kv1 = (x + 1) * plen < nt ? (x + 1) * plen : nt;
+        hu.u[hu.n++] = DenseUnit{a + i, ntok, i, b, x * plen, kv1,
+                                 k > 1 ? slots + x * p.G : -1, a};
+      }
+      if (k > 1) slots += k * p.G;
+    }
+  }
+  if (!one_wave)
+    std::stable_sort(hu.u, hu.u + hu.n, [](const DenseUnit& x, const DenseUnit& y) {
+      return x.kv1 - x.kv0 > y.kv1 - y.kv0;
+    });
+  return true;
+}
+
+// the register split needs exactly the launch budget it was written for
+template <typename K>
+cudaError_t prepare(K kern, int smem) {
+  static_assert(2 * 128 * kRegSoftmax + 128 * kRegOther == (uint32_t)kThreads * kLaunchRegs,
+                "register split must add up to the launch budget");
+  cudaFuncAttributes attr;
+  const cudaError_t e = cudaFuncGetAttributes(&attr, kern);
+  if (e != cudaSuccess) return e;
+  if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
 template <int D>
@@ -880,6 +1157,52 @@ cudaError_t launch_impl(const DensePrefillLaunch& p, cudaStream_t s, int* launch
         !make_tmap_bf16_nd(&mv, paged ? p.cache.v : p.v, 5, dims, str, box))
       return cudaErrorInvalidValue;
   }
+  PrefillArgs a;
+  a.H = p.H;
+  a.G = p.G;
+  a.HG = HG;
+  a.TT = TT;
+  a.scale = p.scale;
+  a.scale_log2 = p.scale * kLog2e;
+  a.units = p.units;
+  a.n_units = p.counts;
+  a.max_units = p.max_units;
+  a.block_table = p.cache.block_table;
+  a.table_stride = p.cache.table_stride;
+  a.page_size = p.cache.page_size;
+  a.num_pages = (int32_t)p.cache.num_pages;
+  a.page_stride = p.cache.page_stride;
+  a.v = static_cast<const __nv_bfloat16*>(paged ? p.cache.v : p.v);
+  a.out = static_cast<__nv_bfloat16*>(p.out);
+  a.part_o = p.part_o;
+  a.part_ml = p.part_ml;
+  a.clear_err = p.clear_err;
+  a.err = p.err;
+  // a warp per row of the split units, as far as there can be rows (those of
+  // tokens that a unit lacks included)
+  const int64_t rows = min64(p.T * p.H + (int64_t)p.B * p.G * 2 * kRows, (int64_t)p.grid * kRows);
+  const int combine_grid = (int)min64((rows + 7) / 8, (int64_t)p.grid * 16);
+
+  HostUnits hu;
+  HostSplits hs;
+  cudaError_t e;
+  if (!p.cu && host_plan(p, TT, hu, hs)) {
+    auto kern = dense_prefill_kernel<D, true>;
+    if ((e = prepare(kern, Cfg::kSmem)) != cudaSuccess) return e;
+    const int grid = (int)min64((int64_t)hu.n * p.G, p.grid);
+    kern<<<grid, kThreads, Cfg::kSmem, s>>>(mq, mk, mv, a, hu);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    ++*launches;
+    if (hs.n > 0) {
+      e = launch_early(dense_combine_kernel<D, true>, combine_grid, 256, 0, s, hs,
+                       (const DenseSplit*)nullptr, (const int32_t*)nullptr, (const float*)p.part_o,
+                       (const float2*)p.part_ml, p.H, p.G, TT, a.out);
+      if (e != cudaSuccess) return e;
+      ++*launches;
+    }
+    return cudaSuccess;
+  }
+
   PlanArgs pl;
   pl.cu = p.cu;
   pl.seq_lens = p.seq_lens;
@@ -890,55 +1213,28 @@ cudaError_t launch_impl(const DensePrefillLaunch& p, cudaStream_t s, int* launch
   pl.table_rows = paged ? (int32_t)min64((int64_t)p.cache.table_stride * p.cache.page_size,
                                          (int64_t)1 << 30)
                         : 0;
-  pl.split_ctas = p.max_slots > 0 ? p.grid : 0;
-  pl.max_slots = p.max_slots;
+  pl.ctas = p.grid;
+  pl.can_split = p.max_slots > 0;
   pl.max_units = p.max_units;
   pl.units = p.units;
   pl.splits = p.splits;
   pl.counts = p.counts;
+  pl.clear_err = p.clear_err;
   pl.err = p.err;
-  dense_plan_kernel<<<1, kPlanThreads, 0, s>>>(*p.offsets, pl);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  // few units: a small block, whose barriers and launch are quicker
+  const int plan_threads = p.T / (2 * TT) + p.B <= 256 ? 256 : kPlanThreads;
+  dense_plan_kernel<<<1, plan_threads, 0, s>>>(*p.offsets, pl);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   ++*launches;
-
-  PrefillArgs a;
-  a.H = p.H;
-  a.G = p.G;
-  a.HG = HG;
-  a.TT = TT;
-  a.scale = p.scale;
-  a.scale_log2 = p.scale * kLog2e;
-  a.units = p.units;
-  a.n_units = p.counts;
-  a.block_table = p.cache.block_table;
-  a.table_stride = p.cache.table_stride;
-  a.page_size = p.cache.page_size;
-  a.num_pages = (int32_t)p.cache.num_pages;
-  a.page_stride = p.cache.page_stride;
-  a.v = static_cast<const __nv_bfloat16*>(paged ? p.cache.v : p.v);
-  a.out = static_cast<__nv_bfloat16*>(p.out);
-  a.part_o = p.part_o;
-  a.part_ml = p.part_ml;
-  a.err = p.err;
-  auto kern = dense_prefill_kernel<D>;
-  // the register split needs exactly the launch budget it was written for
-  cudaFuncAttributes attr;
-  e = cudaFuncGetAttributes(&attr, kern);
-  if (e != cudaSuccess) return e;
-  static_assert(2 * 128 * kRegSoftmax + 128 * kRegOther == (uint32_t)kThreads * kLaunchRegs,
-                "register split must add up to the launch budget");
-  if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
-  if (e != cudaSuccess) return e;
-  kern<<<p.grid, kThreads, Cfg::kSmem, s>>>(mq, mk, mv, a);
-  e = cudaGetLastError();
+  auto kern = dense_prefill_kernel<D, false>;
+  if ((e = prepare(kern, Cfg::kSmem)) != cudaSuccess) return e;
+  e = launch_early(kern, p.grid, kThreads, Cfg::kSmem, s, mq, mk, mv, a, NoHostUnits{});
   if (e != cudaSuccess) return e;
   ++*launches;
   if (p.max_slots > 0) {
-    dense_combine_kernel<D><<<p.grid * 4, 256, 0, s>>>(p.splits, p.counts, p.part_o, p.part_ml,
-                                                       p.H, p.G, TT, a.out);
-    e = cudaGetLastError();
+    e = launch_early(dense_combine_kernel<D, false>, combine_grid, 256, 0, s, NoHostUnits{},
+                     (const DenseSplit*)p.splits, (const int32_t*)p.counts, (const float*)p.part_o,
+                     (const float2*)p.part_ml, p.H, p.G, TT, a.out);
     if (e != cudaSuccess) return e;
     ++*launches;
   }

@@ -253,6 +253,7 @@ struct DensePrefillLaunch {
   float* part_o;
   float2* part_ml;
   int32_t max_units, max_slots;
+  int32_t clear_err;  // clear the error word first
   uint32_t* err;
   int grid;
 };

@@ -492,6 +492,15 @@ __device__ __forceinline__ bool named_barrier_or(uint32_t id, uint32_t count, bo
   return r != 0;
 }
 
+// Programmatic dependent launch: a kernel launched with the attribute may start
+// while the one before it runs, and waits here until that one is complete.
+__device__ __forceinline__ void pdl_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // True in one lane of a converged warp (always the same one).  A branch on it is
 // known to the compiler to hold a single thread, which a test of the lane number
 // is not: tcgen05 instructions in it take their operands straight from uniform
