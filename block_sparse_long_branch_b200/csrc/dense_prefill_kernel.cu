@@ -30,11 +30,13 @@
 // Warp roles (384 threads, one CTA per SM, persistent over the units):
 //   WG0, WG1  softmax of row tile 0 / 1, one thread per row; the rescaling of
 //             O; the cleaning of V; the final O / l;
-//   WG2       warp 8 TMA loads, warp 9 MMA issuer (two warps idle: the register
-//             split goes by warpgroups).
-// TMEM (512 columns): S0, S1 (fp32; each P overwrites the first half of its S)
-// and O0, O1.  While one tile's exponentials are computed the tensor cores work
-// on the other tile.
+//   WG2       warp 8 TMA loads, warp 9 issues S, warp 10 issues PV (one warp
+//             idle: the register split goes by warpgroups).
+// TMEM (512 columns): one S buffer for both row tiles (0-127), P0, P1 (64 columns
+// each) and O0, O1.  A softmax thread copies its row of S into registers at once,
+// so the S buffer is free again for the other tile, whose next S is ready when its
+// warpgroup comes for it.  With an S of its own per tile and P over it, a tile's
+// next S had to wait for its product: 1400 of 3350 cycles per 128 keys.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -47,11 +49,11 @@ namespace msa {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kLoadWarp = 8, kSWarp = 9, kPVWarp = 10;
 constexpr uint32_t kRegSoftmax = 208, kRegOther = 88;
 constexpr int kLaunchRegs = 168;  // 2*128*208 + 128*88 = 384*168
 constexpr int kRows = 128, kKeys = 128;
-constexpr uint32_t kColS = 0, kColO = 256;
+constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;  // log2 of the growth of the maximum left unapplied
 constexpr int kFlagSlots = 8;
@@ -64,9 +66,6 @@ struct PrefillCfg {
   // 224 KiB hold beside the two Q tiles.  A tile takes some 2000 cycles to come
   // from L2; with two K and two V tiles the MMAs waited for it.
   static constexpr int kSlots = D == 128 ? 5 : 10;
-  // P handed over in two parts (96 and 32 keys): 680 against 644 TFLOP/s at d = 64
-  // (8K prompt, 64 heads), nothing gained at d = 128 (1161 against 1176)
-  static constexpr bool kSplitP = D == 64;
   static constexpr int kOffRing = 2 * kTileBytes;
   static constexpr int kSmem = kOffRing + kSlots * kTileBytes + 1024;
 };
@@ -185,7 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t bar_q_full[2], bar_q_empty[2];
   __shared__ uint64_t bar_full[Cfg::kSlots], bar_empty[Cfg::kSlots];
   __shared__ uint64_t bar_clean[2];  // V tiles cleaned, in turn
-  __shared__ uint64_t bar_s_full[2], bar_p_most[2], bar_p_full[2], bar_pv_done[2], bar_drain;
+  __shared__ uint64_t bar_s_full[2], bar_s_empty, bar_p_full[2], bar_pv_done[2];
+  __shared__ uint64_t bar_drain[2];
   __shared__ uint64_t bar_half_done, bar_half_read;  // dual units: tile 1's result, and its reading
   __shared__ float half_m[kRows], half_l[kRows];
   __shared__ uint32_t tmem_base_s;
@@ -200,7 +200,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar_q_empty[i], 1);
       mbar_init(&bar_clean[i], 128);
       mbar_init(&bar_s_full[i], 1);
-      mbar_init(&bar_p_most[i], 128);
       mbar_init(&bar_p_full[i], 128);
       mbar_init(&bar_pv_done[i], 1);
     }
@@ -208,7 +207,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar_full[i], 1);
       mbar_init(&bar_empty[i], 1);
     }
-    mbar_init(&bar_drain, 1);
+    mbar_init(&bar_s_empty, 128);
+    mbar_init(&bar_drain[0], 1);
+    mbar_init(&bar_drain[1], 1);
     mbar_init(&bar_half_done, 128);
     mbar_init(&bar_half_read, 128);
     for (int i = 0; i < kFlagSlots; ++i) odd_v[i] = 0;
@@ -326,18 +327,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t x = loads > Cfg::kSlots ? loads - Cfg::kSlots : 0; x < loads; ++x)
           mbar_wait(&bar_full[x % Cfg::kSlots], (x / Cfg::kSlots) & 1, &no_abort, nullptr, 0);
       }
-    } else if (warp == kMmaWarp) {
-      // ---------------- MMA issuer ----------------
+    } else if (warp == kSWarp || warp == kPVWarp) {
+      // ---------------- MMA issuers ----------------
       // The whole warp walks the units, so that the operands of the MMAs are
       // warp-uniform (uniform registers); one lane issues.  With the walk in
       // one lane alone a batch of eight MMAs took 870 cycles to issue.
-      constexpr uint32_t idesc_s = idesc_bf16(kRows, kKeys, false, false);
-      constexpr uint32_t idesc_o = idesc_bf16(kRows, D, false, true);
       constexpr uint32_t kTile16 = Cfg::kTileBytes / 16;  // descriptor units
-      const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t k_desc = smem_desc_sw128(smem_u32(sR), 16, 1024);
-      const uint64_t v_desc = smem_desc_sw128(smem_u32(sR), kKeys * 128, 1024);
-      uint32_t qn[2] = {0, 0}, pn[2] = {0, 0}, cleaned = 0;
       uint32_t base = 0;  // ring position of the unit's first tile: K_j at base + 2j, V_j after it
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
@@ -352,125 +347,105 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) umma_commit(&bar_empty[slot_of(x)]);
         __syncwarp();
       };
-      auto issue_s = [&](int i, uint32_t x, bool last) {
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t qd = q_desc + (uint32_t)i * kTile16, kd = k_desc + slot_of(x) * kTile16;
+      if (warp == kSWarp) {
+        // S = Q_i K^T of both row tiles in turn, into the one S buffer as soon as
+        // the softmax has copied the S before into its registers
+        constexpr uint32_t idesc_s = idesc_bf16(kRows, kKeys, false, false);
+        const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t k_desc = smem_desc_sw128(smem_u32(sR), 16, 1024);
+        uint32_t qn[2] = {0, 0}, sn = 0;
+        for (int r = 0; r < rounds && ok; ++r) {
+          Unit u;
+          if (!get_unit<HOST>(a, hu, total, r, u)) continue;
+          // broadcasts: known to be the same in every lane
+          const int nt = __shfl_sync(0xffffffffu, u.nt, 0);
+          const int cnt[2] = {__shfl_sync(0xffffffffu, u.c0, 0), __shfl_sync(0xffffffffu, u.c1, 0)};
+          const bool dual = __shfl_sync(0xffffffffu, (int)u.dual, 0) != 0;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * kRows * 128 + (kk & 3) * 32) / 16;
-            umma_bf16(tmem + kColS + i * 128, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
-          }
-          umma_commit(&bar_s_full[i]);
-          if (last) umma_commit(&bar_q_empty[i]);
-        }
-        __syncwarp();
-      };
-      // O_i += P_i V once P_i is there
-      auto issue_pv = [&](int i, uint32_t x, bool first) {
-        const uint64_t vd = v_desc + slot_of(x) * kTile16;
-        auto step = [&](int kk) {  // keys 16kk .. 16kk+15
-          umma_f16_ts(tmem + kColO + i * 128, tmem + kColS + i * 128 + kk * 8,
-                      vd + (uint32_t)(kk * 16 * 128 / 16), idesc_o, (!first || kk > 0) ? 1u : 0u);
-        };
-        if (Cfg::kSplitP) {
-          if (!wait(&bar_p_most[i], pn[i] & 1, kDevTimeoutConsumer)) return;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < 6; ++kk) step(kk);
-          }
-          __syncwarp();
-        }
-        if (!wait(&bar_p_full[i], pn[i] & 1, kDevTimeoutConsumer)) return;
-        ++pn[i];
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = Cfg::kSplitP ? 6 : 0; kk < 8; ++kk) step(kk);
-          umma_commit(&bar_pv_done[i]);
-        }
-        __syncwarp();
-      };
-      // V_j as loaded, or cleaned where some row does not see the whole tile
-      auto wait_v = [&](uint32_t x, bool clean) {
-        if (!clean) return wait_full(x);
-        const uint32_t c = cleaned++;
-        return wait(&bar_clean[c & 1], (c >> 1) & 1, kDevTimeoutConsumer);
-      };
-      for (int r = 0; r < rounds && ok; ++r) {
-        Unit u;
-        if (!get_unit<HOST>(a, hu, total, r, u)) continue;
-        // broadcasts: known to be the same in every lane
-        const int nt = __shfl_sync(0xffffffffu, u.nt, 0);
-        const int cnt[2] = {__shfl_sync(0xffffffffu, u.c0, 0), __shfl_sync(0xffffffffu, u.c1, 0)};
-        const int part0 = __shfl_sync(0xffffffffu, first_partial(u) - u.d.kv0, 0);
-        const bool dual = __shfl_sync(0xffffffffu, (int)u.dual, 0) != 0;
-        if (dual) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (cnt[i] == 0) continue;
-            if (!wait_full(base + 2 * i)) break;
-            if (!wait(&bar_q_full[i], qn[i] & 1, kDevTimeoutLoad)) break;
-            ++qn[i];
-            issue_s(i, base + 2 * i, cnt[i] == 1);
-            free_slot(base + 2 * i);
-          }
-          for (int j = 0; j < nt && ok; j += 2) {
+          for (int i = 0; i < 2; ++i)
+            if (ok && cnt[i] > 0) wait(&bar_q_full[i], qn[i]++ & 1, kDevTimeoutLoad);
+          const int most = max(cnt[0], cnt[1]);
+          for (int j = 0; j < most && ok; ++j) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const int jj = j + i;
-              if (jj >= nt) continue;
-              const uint32_t x = base + 2 * jj;
-              if (!wait_v(x + 1, jj >= part0)) break;
-              issue_pv(i, x + 1, jj < 2);
-              if (!ok) break;
-              free_slot(x + 1);
-              if (jj + 2 < nt) {
-                if (!wait_full(x + 4)) break;
-                issue_s(i, x + 4, jj + 4 >= nt);
-                free_slot(x + 4);
+              if (!ok || j >= cnt[i]) continue;
+              const uint32_t x = base + 2 * (dual ? 2 * j + i : j);
+              if (dual || i == (j < cnt[0] ? 0 : 1)) {
+                if (!wait_full(x)) break;
               }
+              if (!wait(&bar_s_empty, (sn & 1) ^ 1, kDevTimeoutConsumer)) break;
+              ++sn;
+              tc_fence_after();
+              if (elect_one()) {
+                const uint64_t qd = q_desc + (uint32_t)i * kTile16, kd = k_desc + slot_of(x) * kTile16;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint32_t off = ((kk >> 2) * kRows * 128 + (kk & 3) * 32) / 16;
+                  umma_bf16(tmem + kColS, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+                }
+                umma_commit(&bar_s_full[i]);
+                if (j == cnt[i] - 1) umma_commit(&bar_q_empty[i]);
+              }
+              __syncwarp();
+              if (dual || i == (j < cnt[1] ? 1 : 0)) free_slot(x);
             }
           }
-        } else {
-          if (!wait_full(base)) break;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (cnt[i] == 0) continue;
-            if (!wait(&bar_q_full[i], qn[i] & 1, kDevTimeoutLoad)) break;
-            ++qn[i];
-            issue_s(i, base, cnt[i] == 1);
-          }
-          if (!ok) break;
-          free_slot(base);
-          for (int j = 0; j < nt; ++j) {
-            const uint32_t x = base + 2 * j;
-            if (!wait_v(x + 1, j >= part0)) break;
-            if (j + 1 < nt && !wait_full(x + 2)) break;
+          base += 2 * nt;
+        }
+      } else {
+        // O_i += P_i V once P_i is there
+        constexpr uint32_t idesc_o = idesc_bf16(kRows, D, false, true);
+        const uint64_t v_desc = smem_desc_sw128(smem_u32(sR), kKeys * 128, 1024);
+        uint32_t pn[2] = {0, 0}, cleaned = 0;
+        for (int r = 0; r < rounds && ok; ++r) {
+          Unit u;
+          if (!get_unit<HOST>(a, hu, total, r, u)) continue;
+          const int nt = __shfl_sync(0xffffffffu, u.nt, 0);
+          const int cnt[2] = {__shfl_sync(0xffffffffu, u.c0, 0), __shfl_sync(0xffffffffu, u.c1, 0)};
+          const int part0 = __shfl_sync(0xffffffffu, first_partial(u) - u.d.kv0, 0);
+          const bool dual = __shfl_sync(0xffffffffu, (int)u.dual, 0) != 0;
+          const int most = max(cnt[0], cnt[1]);
+          for (int j = 0; j < most && ok; ++j) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              if (j >= cnt[i]) continue;
-              issue_pv(i, x + 1, j == 0);
-              if (!ok) break;
-              if (j + 1 < cnt[i]) issue_s(i, x + 2, j + 2 == cnt[i]);
+              if (!ok || j >= cnt[i]) continue;
+              const int jt = dual ? 2 * j + i : j;
+              const uint32_t x = base + 2 * jt + 1;
+              if (dual || i == (j < cnt[0] ? 0 : 1)) {
+                // V as loaded, or cleaned where some row does not see the whole tile
+                if (jt < part0) {
+                  if (!wait_full(x)) break;
+                } else {
+                  const uint32_t c = cleaned++;
+                  if (!wait(&bar_clean[c & 1], (c >> 1) & 1, kDevTimeoutConsumer)) break;
+                }
+              }
+              if (!wait(&bar_p_full[i], pn[i] & 1, kDevTimeoutConsumer)) break;
+              ++pn[i];
+              tc_fence_after();
+              if (elect_one()) {
+                const uint64_t vd = v_desc + slot_of(x) * kTile16;
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk)  // keys 16kk .. 16kk+15: 8 columns of P
+                  umma_f16_ts(tmem + kColO + i * 128, tmem + kColP + i * 64 + kk * 8,
+                              vd + (uint32_t)(kk * 16 * 128 / 16), idesc_o,
+                              (j > 0 || kk > 0) ? 1u : 0u);
+                umma_commit(&bar_pv_done[i]);
+              }
+              __syncwarp();
+              if (dual || i == (j < cnt[1] ? 1 : 0)) free_slot(x);
             }
-            if (!ok) break;
-            if (elect_one()) {
-              umma_commit(&bar_empty[slot_of(x + 1)]);
-              if (j + 1 < nt) umma_commit(&bar_empty[slot_of(x + 2)]);
-            }
-            __syncwarp();
           }
+          base += 2 * nt;
         }
-        base += 2 * nt;
       }
       // after an abort every product issued must be done before TMEM and shared
-      // memory go; the drain barrier is used for nothing else
+      // memory go; the drain barriers are used for nothing else
       if (*abort_flag && elect_one()) {
         volatile int no_abort = 0;
-        umma_commit(&bar_drain);
-        mbar_wait(&bar_drain, 0, &no_abort, nullptr, 0);
+        uint64_t* drain = &bar_drain[warp - kSWarp];
+        umma_commit(drain);
+        mbar_wait(drain, 0, &no_abort, nullptr, 0);
       }
     }
   } else {
@@ -481,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quarter * 32 + lane;
     const int tt = row / a.HG;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t s_addr = lane_addr + kColS + i * 128;
+    const uint32_t s_addr = lane_addr + kColS;
+    const uint32_t p_addr = lane_addr + kColP + i * 64;
     const uint32_t o_addr = lane_addr + kColO + i * 128;
     const uint64_t k2 = f2_pack(a.scale_log2, a.scale_log2);
     uint32_t sn = 0, pvn = 0, halves = 0;
@@ -565,6 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_32x32b_x32_at<96>(s_addr + 96, s);
         tmem_wait();
         reg_fence(s);
+        tc_fence_before();
+        mbar_arrive(&bar_s_empty);  // the next S may be computed
         if (__any_sync(0xffffffffu, lim < kKeys - 1)) {
 #pragma unroll
           for (int c = 0; c < kKeys; ++c)
@@ -608,30 +586,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float ms = m > -INFINITY ? m * a.scale_log2 : 0.f;
         const uint64_t nm2 = f2_pack(-ms, -ms);
         uint64_t acc_a = f2_pack(0.f, 0.f), acc_b = acc_a;
+        // P in place of the S it comes from: word c of the row's 64 in s[c]
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          uint32_t w[16];
-#pragma unroll
-          for (int x2 = 0; x2 < 16; ++x2) {
-            const int col = 32 * q4 + 2 * x2;
-            const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[col]), __uint_as_float(s[col + 1])),
-                                      k2, nm2);
-            float p0, p1;
-            f2_unpack(x, p0, p1);
-            p0 = fast_exp2(p0), p1 = fast_exp2(p1);
-            w[x2] = pack_bf16x2(p0, p1);
-            if (x2 & 1)
-              acc_b = f2_add(acc_b, f2_pack(p0, p1));
-            else
-              acc_a = f2_add(acc_a, f2_pack(p0, p1));
-          }
-          tmem_st_32x32b_x16(s_addr + 16 * q4, w);
-          if (Cfg::kSplitP && q4 == 2) {  // the product with the first 96 keys' values may start
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&bar_p_most[i]);
-          }
+        for (int c = 0; c < kKeys / 2; ++c) {
+          float p0, p1;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), k2, nm2),
+                    p0, p1);
+          p0 = fast_exp2(p0), p1 = fast_exp2(p1);
+          s[c] = pack_bf16x2(p0, p1);
+          if (c & 1)
+            acc_b = f2_add(acc_b, f2_pack(p0, p1));
+          else
+            acc_a = f2_add(acc_a, f2_pack(p0, p1));
         }
+        // the product of the tile before has read its P by now
+        if (j > 0) {
+          ok = mbar_wait(&bar_pv_done[i], (pvn - 1) & 1, abort_flag, a.err, kDevTimeoutMma);
+          if (!ok) break;
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) tmem_st_32x32b_x16(p_addr + 16 * q4, s + 16 * q4);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bar_p_full[i]);
