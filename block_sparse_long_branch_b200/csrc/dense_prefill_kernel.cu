@@ -30,8 +30,8 @@
 // Warp roles (384 threads, one CTA per SM, persistent over the units):
 //   WG0, WG1  softmax of row tile 0 / 1, one thread per row; the rescaling of
 //             O; the cleaning of V; the final O / l;
-//   WG2       warp 8 TMA loads, warp 9 issues S, warp 10 issues PV (one warp
-//             idle: the register split goes by warpgroups).
+//   WG2       warp 8 loads Q and K, warp 11 V (TMA; with pages of 16 tokens a
+//             tile of 128 keys is 16 copies), warp 9 issues S, warp 10 issues PV.
 // TMEM (512 columns): one S buffer for both row tiles (0-127), P0, P1 (64 columns
 // each) and O0, O1.  A softmax thread copies its row of S into registers at once,
 // so the S buffer is free again for the other tile, whose next S is ready when its
@@ -49,7 +49,7 @@ namespace msa {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kLoadWarp = 8, kSWarp = 9, kPVWarp = 10;
+constexpr int kLoadWarp = 8, kSWarp = 9, kPVWarp = 10, kLoadVWarp = 11;
 constexpr uint32_t kRegSoftmax = 208, kRegOther = 88;
 constexpr int kLaunchRegs = 168;  // 2*128*208 + 128*88 = 384*168
 constexpr int kRows = 128, kKeys = 128;
@@ -57,26 +57,20 @@ constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;  // log2 of the growth of the maximum left unapplied
 constexpr int kFlagSlots = 8;
+constexpr int kTurns = 8;
+constexpr int kBoxRows = 128;  // of a TMA copy, at most (smaller boxes gained nothing)
 
 template <int D>
 struct PrefillCfg {
   static constexpr int kChunks = D / 64;           // 128-byte column chunks
   static constexpr int kTileBytes = kRows * D * 2;  // Q, K and V tiles alike
-  // one ring for K and V tiles in the order of their use (K0 V0 K1 V1 ...): what
+  // Rings of K and of V tiles, each filled and emptied in its own order: what
   // 224 KiB hold beside the two Q tiles.  A tile takes some 2000 cycles to come
-  // from L2; with two K and two V tiles the MMAs waited for it.
-  static constexpr int kSlots = D == 128 ? 5 : 10;
-  static constexpr int kOffRing = 2 * kTileBytes;
-  static constexpr int kSmem = kOffRing + kSlots * kTileBytes + 1024;
-};
-
-// position in the ring: slot and the parity of its use
-template <int N>
-struct Ring {
-  uint32_t slot = 0, phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++slot == N) slot = 0, phase ^= 1;
-  }
+  // from L2.
+  static constexpr int kKSlots = D == 128 ? 3 : 5, kVSlots = D == 128 ? 2 : 5;
+  static constexpr int kOffK = 2 * kTileBytes;
+  static constexpr int kOffV = kOffK + kKSlots * kTileBytes;
+  static constexpr int kSmem = kOffV + kVSlots * kTileBytes + 1024;
 };
 
 struct PrefillArgs {
@@ -88,6 +82,7 @@ struct PrefillArgs {
   // paged keys and values; page_size 0: packed rows
   const int32_t* block_table;
   int32_t table_stride, page_size, num_pages;
+  int32_t box_rows;     // of a TMA copy of keys or values
   int64_t page_stride;  // elements
   const __nv_bfloat16* v;
   __nv_bfloat16* out;
@@ -180,10 +175,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;
-  uint8_t* sR = smem + Cfg::kOffRing;
+  uint8_t* sK = smem + Cfg::kOffK;
+  uint8_t* sV = smem + Cfg::kOffV;
+  constexpr uint32_t KS = Cfg::kKSlots, VS = Cfg::kVSlots;
   __shared__ uint64_t bar_q_full[2], bar_q_empty[2];
-  __shared__ uint64_t bar_full[Cfg::kSlots], bar_empty[Cfg::kSlots];
-  __shared__ uint64_t bar_clean[2];  // V tiles cleaned, in turn
+  // A wait for a phase's parity is right only while the phase before it is known
+  // to be complete.  So every barrier is waited on by one warp (or warpgroup) use
+  // by use, or (bar_spec, bar_clean) in turns that the steps around them order.
+  __shared__ uint64_t bar_k_full[KS], bar_k_empty[KS], bar_v_empty[VS];
+  // V tiles that every row sees whole, in turn; and the others, "special" ones:
+  // loaded, and cleaned
+  __shared__ uint64_t bar_v_full[VS], bar_spec[VS], bar_clean[kTurns];
   __shared__ uint64_t bar_s_full[2], bar_s_empty, bar_p_full[2], bar_pv_done[2];
   __shared__ uint64_t bar_drain[2];
   __shared__ uint64_t bar_half_done, bar_half_read;  // dual units: tile 1's result, and its reading
@@ -198,15 +200,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_q_full[i], 1);
       mbar_init(&bar_q_empty[i], 1);
-      mbar_init(&bar_clean[i], 128);
       mbar_init(&bar_s_full[i], 1);
       mbar_init(&bar_p_full[i], 128);
       mbar_init(&bar_pv_done[i], 1);
     }
-    for (int i = 0; i < Cfg::kSlots; ++i) {
-      mbar_init(&bar_full[i], 1);
-      mbar_init(&bar_empty[i], 1);
+    for (uint32_t i = 0; i < KS; ++i) {
+      mbar_init(&bar_k_full[i], 1);
+      mbar_init(&bar_k_empty[i], 1);
     }
+    for (uint32_t i = 0; i < VS; ++i) {
+      mbar_init(&bar_v_full[i], 1);
+      mbar_init(&bar_spec[i], 1);
+      mbar_init(&bar_v_empty[i], 1);
+    }
+    for (int i = 0; i < kTurns; ++i) mbar_init(&bar_clean[i], 128);
     mbar_init(&bar_s_empty, 128);
     mbar_init(&bar_drain[0], 1);
     mbar_init(&bar_drain[1], 1);
@@ -243,16 +250,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
     regs_decrease<kRegOther>();
-    if (warp == kLoadWarp) {
-      // ---------------- TMA loads ----------------
-      Ring<Cfg::kSlots> ring;
-      uint32_t loads = 0;         // copies into the ring so far
-      uint32_t qn[2] = {0, 0};    // Q tiles loaded so far
+    if (warp == kLoadWarp || warp == kLoadVWarp) {
+      // ---------------- TMA loads: Q and K, or V ----------------
+      const bool is_v = warp == kLoadVWarp;
+      const CUtensorMap* map = is_v ? &map_v : &map_k;
+      const uint32_t slots = is_v ? VS : KS;
+      uint64_t* empty = is_v ? bar_v_empty : bar_k_empty;
+      uint8_t* ring = is_v ? sV : sK;
+      uint32_t slot = 0, phase = 0;       // of the next tile
+      uint32_t regular = 0, special = 0;  // V tiles of both kinds so far
+      uint64_t* last_full = nullptr;     // of the last copy
+      uint32_t last_par = 0;
+      uint32_t qn[2] = {0, 0};      // Q tiles loaded so far
       bool ok = true;
-      const int boxes = a.page_size == 0 ? 1 : (a.page_size >= kKeys ? 1 : kKeys / a.page_size);
-      const int box_rows = kKeys / boxes;
+      const int box_rows = a.box_rows, boxes = kKeys / box_rows;  // a lane per box of a tile
       auto load_q = [&](const Unit& u, int i) {
-        if (!ok || (i == 0 ? u.c0 : u.c1) == 0) return;
+        if (!ok || is_v || (i == 0 ? u.c0 : u.c1) == 0) return;
         if (lane == 0) {
           ok = mbar_wait(&bar_q_empty[i], (qn[i] & 1) ^ 1, abort_flag, a.err, kDevTimeoutMma);
           if (ok) {
@@ -266,31 +279,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (ok) ++qn[i];
       };
-      // the next tile into the ring: one box per page, a lane each; pages past
-      // the sequence's end are not read
-      auto load_kv = [&](const CUtensorMap* map, int g, int32_t row, int32_t page, int nbox) {
-        if (!ok) return;
-        uint64_t* full = &bar_full[ring.slot];
-        if (lane == 0) {
-          ok = mbar_wait(&bar_empty[ring.slot], ring.phase ^ 1, abort_flag, a.err, kDevTimeoutMma);
-          if (ok) mbar_arrive_expect_tx(full, (uint32_t)(nbox * box_rows * D * 2));
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) return;
-        if (lane < nbox) {
-          uint8_t* dst = sR + ring.slot * Cfg::kTileBytes + lane * box_rows * 128;
-#pragma unroll
-          for (int c = 0; c < Cfg::kChunks; ++c)
-            tma_load_5d(dst + c * kKeys * 128, map, full, 0, row, c, g, page);
-        }
-        __syncwarp();
-        ++loads;
-        ring.next();
-      };
       for (int r = 0; r < rounds && ok; ++r) {
         Unit u;
         if (!get_unit<HOST>(a, hu, total, r, u)) continue;
         const int keys_end = u.d.pos0 + u.d.ntok;
+        const int part0 = first_partial(u) - u.d.kv0;
         // lane i: page of box i of a key tile (0: none, or packed rows)
         auto page_of = [&](int j) {
           const int key = (u.d.kv0 + j) * kKeys + lane * box_rows;
@@ -302,11 +295,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int key0 = (u.d.kv0 + j) * kKeys;
           int page = page_next;
           page_next = page_of(j + 1);  // its latency behind this tile's waits
-          int32_t row = u.d.row0 + key0;
-          int nbox = 1;
+          // boxes past the sequence's end are not read
+          const int left = (keys_end - key0 + box_rows - 1) / box_rows;
+          const int nbox = left < boxes ? left : boxes;
+          int32_t row = u.d.row0 + key0 + lane * box_rows;
           if (a.page_size != 0) {
-            const int left = (keys_end - key0 + box_rows - 1) / box_rows;
-            nbox = left < boxes ? left : boxes;
             row = (key0 + lane * box_rows) % a.page_size;
             if (lane < nbox && (page < 0 || page >= a.num_pages)) {
               record_error(a.err, kDevBadIndex);
@@ -314,9 +307,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (j == 0) load_q(u, 0);
-          load_kv(&map_k, u.g, row, page, nbox);
+          if (!ok) break;
+          uint64_t* full;
+          uint32_t par;
+          if (!is_v) {
+            full = &bar_k_full[slot];
+            par = phase;
+          } else if (j < part0) {
+            full = &bar_v_full[regular % VS];
+            par = (regular++ / VS) & 1;
+          } else {
+            full = &bar_spec[special % VS];
+            par = (special++ / VS) & 1;
+          }
+          if (lane == 0) {
+            ok = mbar_wait(&empty[slot], phase ^ 1, abort_flag, a.err, kDevTimeoutMma);
+            if (ok) mbar_arrive_expect_tx(full, (uint32_t)(nbox * box_rows * D * 2));
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          last_full = full;
+          last_par = par;
+          if (lane < nbox) {
+            uint8_t* dst = ring + slot * Cfg::kTileBytes + lane * box_rows * 128;
+#pragma unroll
+            for (int c = 0; c < Cfg::kChunks; ++c)
+              tma_load_5d(dst + c * kKeys * 128, map, full, 0, row, c, u.g, page);
+          }
+          __syncwarp();
+          if (++slot == slots) slot = 0, phase ^= 1;
           if (j == 0) load_q(u, 1);
-          load_kv(&map_v, u.g, row, page, nbox);
         }
       }
       if (lane == 0 && *abort_flag) {
@@ -324,8 +344,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         volatile int no_abort = 0;
         for (int i = 0; i < 2; ++i)
           if (qn[i]) mbar_wait(&bar_q_full[i], (qn[i] - 1) & 1, &no_abort, nullptr, 0);
-        for (uint32_t x = loads > Cfg::kSlots ? loads - Cfg::kSlots : 0; x < loads; ++x)
-          mbar_wait(&bar_full[x % Cfg::kSlots], (x / Cfg::kSlots) & 1, &no_abort, nullptr, 0);
+        if (last_full) mbar_wait(last_full, last_par, &no_abort, nullptr, 0);
+        for (uint32_t i = 0; i < slots; ++i) {
+          // whichever copies are behind the last one: a microsecond or two
+          const uint64_t t0 = global_timer_ns();
+          while (global_timer_ns() - t0 < 20000) {
+          }
+        }
       }
     } else if (warp == kSWarp || warp == kPVWarp) {
       // ---------------- MMA issuers ----------------
@@ -333,32 +358,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       // warp-uniform (uniform registers); one lane issues.  With the walk in
       // one lane alone a batch of eight MMAs took 870 cycles to issue.
       constexpr uint32_t kTile16 = Cfg::kTileBytes / 16;  // descriptor units
-      uint32_t base = 0;  // ring position of the unit's first tile: K_j at base + 2j, V_j after it
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
         ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err, code));
         return ok;
-      };
-      auto slot_of = [&](uint32_t x) { return x % Cfg::kSlots; };
-      auto wait_full = [&](uint32_t x) {
-        return wait(&bar_full[slot_of(x)], (x / Cfg::kSlots) & 1, kDevTimeoutLoad);
-      };
-      auto free_slot = [&](uint32_t x) {
-        if (elect_one()) umma_commit(&bar_empty[slot_of(x)]);
-        __syncwarp();
       };
       if (warp == kSWarp) {
         // S = Q_i K^T of both row tiles in turn, into the one S buffer as soon as
         // the softmax has copied the S before into its registers
         constexpr uint32_t idesc_s = idesc_bf16(kRows, kKeys, false, false);
         const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-        const uint64_t k_desc = smem_desc_sw128(smem_u32(sR), 16, 1024);
+        const uint64_t k_desc = smem_desc_sw128(smem_u32(sK), 16, 1024);
         uint32_t qn[2] = {0, 0}, sn = 0;
+        uint32_t slot = 0, phase = 0;  // of the K tile
         for (int r = 0; r < rounds && ok; ++r) {
           Unit u;
           if (!get_unit<HOST>(a, hu, total, r, u)) continue;
           // broadcasts: known to be the same in every lane
-          const int nt = __shfl_sync(0xffffffffu, u.nt, 0);
           const int cnt[2] = {__shfl_sync(0xffffffffu, u.c0, 0), __shfl_sync(0xffffffffu, u.c1, 0)};
           const bool dual = __shfl_sync(0xffffffffu, (int)u.dual, 0) != 0;
 #pragma unroll
@@ -369,15 +385,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               if (!ok || j >= cnt[i]) continue;
-              const uint32_t x = base + 2 * (dual ? 2 * j + i : j);
               if (dual || i == (j < cnt[0] ? 0 : 1)) {
-                if (!wait_full(x)) break;
+                if (!wait(&bar_k_full[slot], phase, kDevTimeoutLoad)) break;
               }
               if (!wait(&bar_s_empty, (sn & 1) ^ 1, kDevTimeoutConsumer)) break;
               ++sn;
               tc_fence_after();
               if (elect_one()) {
-                const uint64_t qd = q_desc + (uint32_t)i * kTile16, kd = k_desc + slot_of(x) * kTile16;
+                const uint64_t qd = q_desc + (uint32_t)i * kTile16, kd = k_desc + slot * kTile16;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                   const uint32_t off = ((kk >> 2) * kRows * 128 + (kk & 3) * 32) / 16;
@@ -387,20 +402,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (j == cnt[i] - 1) umma_commit(&bar_q_empty[i]);
               }
               __syncwarp();
-              if (dual || i == (j < cnt[1] ? 1 : 0)) free_slot(x);
+              if (dual || i == (j < cnt[1] ? 1 : 0)) {  // the tile's last use
+                if (elect_one()) umma_commit(&bar_k_empty[slot]);
+                __syncwarp();
+                if (++slot == KS) slot = 0, phase ^= 1;
+              }
             }
           }
-          base += 2 * nt;
         }
       } else {
         // O_i += P_i V once P_i is there
         constexpr uint32_t idesc_o = idesc_bf16(kRows, D, false, true);
-        const uint64_t v_desc = smem_desc_sw128(smem_u32(sR), kKeys * 128, 1024);
-        uint32_t pn[2] = {0, 0}, cleaned = 0;
+        const uint64_t v_desc = smem_desc_sw128(smem_u32(sV), kKeys * 128, 1024);
+        uint32_t pn[2] = {0, 0}, regular = 0, special = 0;
+        uint32_t slot = 0;  // of the V tile
         for (int r = 0; r < rounds && ok; ++r) {
           Unit u;
           if (!get_unit<HOST>(a, hu, total, r, u)) continue;
-          const int nt = __shfl_sync(0xffffffffu, u.nt, 0);
           const int cnt[2] = {__shfl_sync(0xffffffffu, u.c0, 0), __shfl_sync(0xffffffffu, u.c1, 0)};
           const int part0 = __shfl_sync(0xffffffffu, first_partial(u) - u.d.kv0, 0);
           const bool dual = __shfl_sync(0xffffffffu, (int)u.dual, 0) != 0;
@@ -409,22 +427,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               if (!ok || j >= cnt[i]) continue;
-              const int jt = dual ? 2 * j + i : j;
-              const uint32_t x = base + 2 * jt + 1;
               if (dual || i == (j < cnt[0] ? 0 : 1)) {
                 // V as loaded, or cleaned where some row does not see the whole tile
-                if (jt < part0) {
-                  if (!wait_full(x)) break;
+                if ((dual ? 2 * j + i : j) < part0) {
+                  const uint32_t n = regular++;
+                  if (!wait(&bar_v_full[n % VS], (n / VS) & 1, kDevTimeoutLoad)) break;
                 } else {
-                  const uint32_t c = cleaned++;
-                  if (!wait(&bar_clean[c & 1], (c >> 1) & 1, kDevTimeoutConsumer)) break;
+                  const uint32_t n = special++;
+                  if (!wait(&bar_clean[n % kTurns], (n / kTurns) & 1, kDevTimeoutConsumer)) break;
                 }
               }
               if (!wait(&bar_p_full[i], pn[i] & 1, kDevTimeoutConsumer)) break;
               ++pn[i];
               tc_fence_after();
               if (elect_one()) {
-                const uint64_t vd = v_desc + slot_of(x) * kTile16;
+                const uint64_t vd = v_desc + slot * kTile16;
 #pragma unroll
                 for (int kk = 0; kk < kKeys / 16; ++kk)  // keys 16kk .. 16kk+15: 8 columns of P
                   umma_f16_ts(tmem + kColO + i * 128, tmem + kColP + i * 64 + kk * 8,
@@ -433,19 +450,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma_commit(&bar_pv_done[i]);
               }
               __syncwarp();
-              if (dual || i == (j < cnt[1] ? 1 : 0)) free_slot(x);
+              if (dual || i == (j < cnt[1] ? 1 : 0)) {  // the tile's last use
+                if (elect_one()) umma_commit(&bar_v_empty[slot]);
+                __syncwarp();
+                if (++slot == VS) slot = 0;
+              }
             }
           }
-          base += 2 * nt;
         }
       }
-      // after an abort every product issued must be done before TMEM and shared
-      // memory go; the drain barriers are used for nothing else
-      if (*abort_flag && elect_one()) {
+      // every product and commit must be done before TMEM and shared memory go
+      if (elect_one()) {
         volatile int no_abort = 0;
         uint64_t* drain = &bar_drain[warp - kSWarp];
         umma_commit(drain);
-        mbar_wait(drain, 0, &no_abort, nullptr, 0);
+        mbar_wait(drain, 0, &no_abort, a.err, kDevTimeoutMma);
       }
     }
   } else {
@@ -462,21 +481,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t k2 = f2_pack(a.scale_log2, a.scale_log2);
     uint32_t sn = 0, pvn = 0, halves = 0;
     int n = 0;
-    uint32_t base = 0;  // ring position of the unit's first tile
-    uint32_t cleaned = 0;  // V tiles cleaned in the units before
+    uint32_t base = 0;     // V tiles of the units before
+    uint32_t cleaned = 0;  // special ones of them
     int prev_nt = 0, prev_special = 0;
     bool ok = true;
     // Takes infinities and NaNs, and rows past the sequence's end, out of V tile
     // j of a unit.
-    auto clean = [&](const Unit& u, int j, int flag_slot) {
-      const uint32_t x = base + 2 * j + 1;
-      const uint32_t slot = x % Cfg::kSlots;
-      if (!mbar_wait(&bar_full[slot], (x / Cfg::kSlots) & 1, abort_flag, a.err, kDevTimeoutLoad))
+    auto clean = [&](const Unit& u, int j, uint32_t n, int flag_slot) {  // n: special ones before
+      const uint32_t slot = (base + j) % VS;
+      if (!mbar_wait(&bar_spec[n % VS], (n / VS) & 1, abort_flag, a.err, kDevTimeoutLoad))
         return false;
       const int key0 = (u.d.kv0 + j) * kKeys, keys_end = u.d.pos0 + u.d.ntok;
       // 16-byte pieces, 8 per 128-byte line, lines chunk-major; where a piece
       // lies within its line does not matter
-      uint4* tile = reinterpret_cast<uint4*>(sR + slot * Cfg::kTileBytes);
+      uint4* tile = reinterpret_cast<uint4*>(sV + slot * Cfg::kTileBytes);
       bool odd = false;
 #pragma unroll 4
       for (int q = (int)threadIdx.x & 127; q < Cfg::kTileBytes / 16; q += 128) {
@@ -505,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int r = 0; r < rounds && ok; ++r) {
       Unit u;
       if (!get_unit<HOST>(a, hu, total, r, u)) continue;
-      base += 2 * prev_nt;
+      base += prev_nt;
       cleaned += prev_special;
       const int part0 = first_partial(u) - u.d.kv0;
       prev_nt = u.nt;
@@ -525,9 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // While S is on its way: clean V, where some row does not see all of it.
         // One warpgroup does, the first that takes the tile.
         if (jt >= part0 && (i == 0 || u.dual || jt >= u.c0)) {
-          ok = clean(u, jt, flag_slot);
+          const uint32_t n = cleaned + jt - max(part0, 0);
+          ok = clean(u, jt, n, flag_slot);
           if (!ok) break;
-          mbar_arrive(&bar_clean[(cleaned + jt - max(part0, 0)) & 1]);
+          mbar_arrive(&bar_clean[n % kTurns]);
         }
         const int lim = valid ? pos - kt * kKeys : kKeys;
         ok = mbar_wait(&bar_s_full[i], sn & 1, abort_flag, a.err, kDevTimeoutMma);
@@ -753,6 +772,14 @@ __device__ __forceinline__ int bucket_of(int tiles) {  // longer first; tiles >=
   return kBuckets - 1 - (e * 8 + f);
 }
 
+// First key tile of part k of `parts` of a unit of nt key tiles.  The last part has
+// two tiles at least, so that row tile 0, which may end a key tile before row tile
+// 1, has keys in every part.
+__host__ __device__ __forceinline__ int part_begin(int k, int parts, int len, int nt) {
+  if (k >= parts) return nt;
+  return k > 0 && k * len > nt - 2 ? nt - 2 : k * len;
+}
+
 struct PlanArgs {
   const int64_t* cu;          // device offsets of the new tokens, or null: `off`
   const int32_t* seq_lens;    // device, null: whole prompts
@@ -871,7 +898,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     for_units([&](int, int64_t, int, int ntok, int, int nt) {
       int len;
       const int parts = parts_of(ntok, nt, len);
-      for (int k = 0; k < parts; ++k) atomicAdd(&hist[bucket_of(min(len, nt - k * len))], 1);
+      for (int k = 0; k < parts; ++k)
+        atomicAdd(&hist[bucket_of(part_begin(k + 1, parts, len, nt) - part_begin(k, parts, len, nt))], 1);
     });
     __syncthreads();
     if (tid < 32) {  // exclusive prefix over the buckets
@@ -901,12 +929,12 @@ __global__ void __launch_bounds__(kPlanThreads)
       *reinterpret_cast<int4*>(p.splits + x) = make_int4((int)a + i, ntok, slot, parts);
     }
     for (int k = 0; k < parts; ++k) {
-      const int kv1 = min(nt, (k + 1) * len);
-      const int x = one_wave ? atomicAdd(&hist[0], 1) : atomicAdd(&hist[bucket_of(kv1 - k * len)], 1);
+      const int kv0 = part_begin(k, parts, len, nt), kv1 = part_begin(k + 1, parts, len, nt);
+      const int x = one_wave ? atomicAdd(&hist[0], 1) : atomicAdd(&hist[bucket_of(kv1 - kv0)], 1);
       if (x < p.max_units) {
         int4* dst = reinterpret_cast<int4*>(p.units + x);
         dst[0] = make_int4((int)a + i, ntok, pos0, b);
-        dst[1] = make_int4(k * len, kv1, slot < 0 ? -1 : slot + k * p.G,
+        dst[1] = make_int4(kv0, kv1, slot < 0 ? -1 : slot + k * p.G,
                            p.seq_lens ? 0 : (int)a);
       }
     }
@@ -1082,8 +1110,8 @@ bool host_plan(const DensePrefillLaunch& p, int TT, HostUnits& hu, HostSplits& h
       if (hu.n + k > kHostUnits || (k > 1 && hs.n == kHostUnits / 2)) return false;
       if (k > 1) hs.s[hs.n++] = DenseSplit{a + i, ntok, slots, k};
       for (int x = 0; x < k; ++x) {
-        const int kv1 = (x + 1) * plen < nt ? (x + 1) * plen : nt;
-        hu.u[hu.n++] = DenseUnit{a + i, ntok, i, b, x * plen, kv1,
+        hu.u[hu.n++] = DenseUnit{a + i, ntok, i, b, part_begin(x, k, plen, nt),
+                                 part_begin(x + 1, k, plen, nt),
                                  k > 1 ? slots + x * p.G : -1, a};
       }
       if (k > 1) slots += k * p.G;
@@ -1116,7 +1144,7 @@ cudaError_t launch_impl(const DensePrefillLaunch& p, cudaStream_t s, int* launch
   CUtensorMap mq, mk, mv;
   const uint64_t GD = (uint64_t)p.G * D, HD = (uint64_t)p.H * D;
   const bool paged = p.cache.page_size > 0;
-  const int rows_box = paged && p.cache.page_size < kKeys ? p.cache.page_size : kKeys;
+  const int rows_box = paged && p.cache.page_size < kBoxRows ? p.cache.page_size : kBoxRows;
   {
     const uint64_t dims[4] = {64, (uint64_t)p.H, D / 64, (uint64_t)p.T};
     const uint64_t str[3] = {D, 64, HD};
@@ -1147,6 +1175,7 @@ cudaError_t launch_impl(const DensePrefillLaunch& p, cudaStream_t s, int* launch
   a.page_size = p.cache.page_size;
   a.num_pages = (int32_t)p.cache.num_pages;
   a.page_stride = p.cache.page_stride;
+  a.box_rows = rows_box;
   a.v = static_cast<const __nv_bfloat16*>(paged ? p.cache.v : p.v);
   a.out = static_cast<__nv_bfloat16*>(p.out);
   a.part_o = p.part_o;
