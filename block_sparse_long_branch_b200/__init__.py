@@ -685,16 +685,19 @@ def _place(t, stream):
     return index, raw, None if raw == current else stream
 
 
-def _empty(shape, like, side, dtype=torch.bfloat16):
+def _empty_like(t, side):
+    """A contiguous tensor like t for a call on the current stream or on `side`."""
     if side is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
     with torch.cuda.stream(side):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _scratch(ws, cfg, op, T, B, like, side):
     if ws is None:
-        return _empty((msa_workspace_size(cfg, op, T, B),), like, side, torch.uint8)
+        n = msa_workspace_size(cfg, op, T, B)
+        with torch.cuda.stream(side):  # None: the current stream
+            return torch.empty((n,), dtype=torch.uint8, device=like.device)
     if ws.dtype is not torch.uint8 or not ws.is_contiguous() or ws.get_device() != like.get_device():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {like.device}")
     return ws
@@ -744,7 +747,7 @@ def msa_rope_append_paged(cfg: MsaConfig, q, k, v, inv_freq, kv: PagedKV, cu_seq
     if q is not None:
         qp, qs = _rows(q, "q", (T, H, d), index)
         if q_out is None:
-            q_out = _empty((T, H, d), k, side)
+            q_out = _empty_like(q, side)
             op = q_out.data_ptr()
         else:
             op = _arg(q_out, torch.bfloat16, (T, H, d), index, "q_out")
@@ -769,7 +772,7 @@ def msa_dense_prefill_varlen(cfg: MsaConfig, q, k, v, cu_seqlens,
     lib = load_library()
     if hasattr(cu_seqlens, "tolist"):  # a tensor or an array
         cu_seqlens = cu_seqlens.tolist()
-    cu = (ctypes.c_int64 * len(cu_seqlens))(*cu_seqlens)
+    cu = (ctypes.c_int64 * len(cu_seqlens))(*map(int, cu_seqlens))
     B = len(cu) - 1
     index, raw, side = _place(q, stream)
     T = q.shape[0]
@@ -777,11 +780,12 @@ def msa_dense_prefill_varlen(cfg: MsaConfig, q, k, v, cu_seqlens,
     if B < 1 or cu[B] != T:
         raise ValueError(f"cu_seqlens must end at the packed length {T}")
     bf = torch.bfloat16
+    qp = _arg(q, bf, (T, H, d), index, "q")
     if out is None:
-        out = _empty((T, H, d), q, side)
+        out = _empty_like(q, side)
     ws = _scratch(workspace, cfg, OP_DENSE_PREFILL, T, B, q, side)
-    _launch(lib.msa_dense_prefill_varlen, index, "msa_dense_prefill_varlen", ctypes.byref(cfg),
-            _arg(q, bf, (T, H, d), index, "q"), _arg(k, bf, (T, G, d), index, "k"),
+    _launch(lib.msa_dense_prefill_varlen, index, "msa_dense_prefill_varlen", ctypes.byref(cfg), qp,
+            _arg(k, bf, (T, G, d), index, "k"),
             _arg(v, bf, (T, G, d), index, "v"), cu, B, _arg(out, bf, (T, H, d), index, "out"),
             ws.data_ptr(), ws.numel(), raw)
     return out
@@ -800,11 +804,12 @@ def msa_dense_prefill_paged(cfg: MsaConfig, q, kv: PagedKV, cu_seqlens, seq_lens
     H, d = cfg.num_heads, cfg.head_dim
     B = seq_lens.shape[0]
     _kv_check(cfg, kv, B, index)
+    qp = _arg(q, torch.bfloat16, (T, H, d), index, "q")
     if out is None:
-        out = _empty((T, H, d), q, side)
+        out = _empty_like(q, side)
     ws = _scratch(workspace, cfg, OP_DENSE_PREFILL_PAGED, T, B, q, side)
-    _launch(lib.msa_dense_prefill_paged, index, "msa_dense_prefill_paged", ctypes.byref(cfg),
-            _arg(q, torch.bfloat16, (T, H, d), index, "q"), kv.ref,
+    _launch(lib.msa_dense_prefill_paged, index, "msa_dense_prefill_paged", ctypes.byref(cfg), qp,
+            kv.ref,
             _arg(cu_seqlens, torch.int64, (B + 1,), index, "cu_seqlens"),
             _arg(seq_lens, torch.int32, (B,), index, "seq_lens"), B, T,
             _arg(out, torch.bfloat16, (T, H, d), index, "out"), ws.data_ptr(), ws.numel(), raw)
@@ -822,11 +827,12 @@ def msa_dense_decode_paged(cfg: MsaConfig, q, kv: PagedKV, seq_lens,
     B = q.shape[0]
     H, d = cfg.num_heads, cfg.head_dim
     _kv_check(cfg, kv, B, index)
+    qp = _arg(q, torch.bfloat16, (B, H, d), index, "q")
     if out is None:
-        out = _empty((B, H, d), q, side)
+        out = _empty_like(q, side)
     ws = _scratch(workspace, cfg, OP_DENSE_DECODE, B, B, q, side)
-    _launch(lib.msa_dense_decode_paged, index, "msa_dense_decode_paged", ctypes.byref(cfg),
-            _arg(q, torch.bfloat16, (B, H, d), index, "q"), kv.ref,
+    _launch(lib.msa_dense_decode_paged, index, "msa_dense_decode_paged", ctypes.byref(cfg), qp,
+            kv.ref,
             _arg(seq_lens, torch.int32, (B,), index, "seq_lens"), B,
             _arg(out, torch.bfloat16, (B, H, d), index, "out"), ws.data_ptr(), ws.numel(), raw)
     return out

@@ -11,6 +11,8 @@ namespace {
 // CTAs of the persistent kernels, at most; sizes the partial results in the
 // workspace without asking the device (a B200 has 148 SMs)
 constexpr int kMaxCtas = 160;
+// a unit of the prefill is split only when it has more than four key tiles
+constexpr int kSplitKeys = 4 * 128;
 constexpr int kMaxHeadsPerGroup = 128;  // a token's heads of one group fill at most one row tile
 
 int grid_ctas() {
@@ -69,9 +71,7 @@ struct PrefillWs {
 PrefillWs prefill_ws(const msa_config_t* c, int64_t T, int32_t B, bool paged) {
   PrefillWs w;
   const int64_t U = 2 * dense_tile_tokens(c->num_heads, c->num_groups);
-  // a unit is split only when it has more than four key tiles, so packed prompts
-  // of up to 512 tokens never are
-  w.max_slots = paged || T > 4 * 128 ? 2 * kMaxCtas : 0;
+  w.max_slots = paged || T > kSplitKeys ? 2 * kMaxCtas : 0;
   w.max_units = (int32_t)(T / U + B + w.max_slots);
   size_t off = kHeader;
   w.units = off;
@@ -254,10 +254,12 @@ msa_status_t msa_dense_prefill_paged(const msa_config_t* cfg, const void* q,
     return MSA_ERR_INVALID_ARG;
   DensePrefillLaunch p{};
   if ((st = check_cache(cfg, cache, &p.cache)) != MSA_OK) return st;
-  const PrefillWs w = prefill_ws(cfg, T, B, true);
+  PrefillWs w = prefill_ws(cfg, T, B, true);
   if (!ws || !aligned16(ws) || ws_bytes < w.total) return MSA_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   p.clear_err = 1;
+  // no sequence can be long enough to be split: no pass that joins parts
+  if ((int64_t)p.cache.table_stride * p.cache.page_size <= kSplitKeys) w.max_slots = 0;
   static const DenseOffsets kNoOffsets = {};
   p.q = q;
   p.out = out;

@@ -30,7 +30,7 @@
 // Warp roles (384 threads, one CTA per SM, persistent over the units):
 //   WG0, WG1  softmax of row tile 0 / 1, one thread per row; the rescaling of
 //             O; the cleaning of V; the final O / l;
-//   WG2       warp 8 loads Q and K, warp 11 V (TMA; with pages of 16 tokens a
+//   WG2       warp 8 loads K, warp 11 Q and V (TMA; with pages of 16 tokens a
 //             tile of 128 keys is 16 copies), warp 9 issues S, warp 10 issues PV.
 // TMEM (512 columns): one S buffer for both row tiles (0-127), P0, P1 (64 columns
 // each) and O0, O1.  A softmax thread copies its row of S into registers at once,
@@ -58,6 +58,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;  // log2 of the growth of the maximum left unapplied
 constexpr int kFlagSlots = 8;
 constexpr int kTurns = 8;
+constexpr int kDirectUnits = 160;  // as many as CTAs; a multiple of 32
 constexpr int kBoxRows = 128;  // of a TMA copy, at most (smaller boxes gained nothing)
 
 template <int D>
@@ -95,6 +96,7 @@ struct PrefillArgs {
 // The units of a small batch whose lengths the host knows travel as a kernel
 // parameter: no planning kernel in front (prefill of 128 tokens: 14.4 -> 8.5 us).
 constexpr int kHostUnits = 128;
+enum PlanMode { kPlanned, kHost, kDirect };
 struct HostUnits {
   int32_t n;
   DenseUnit u[kHostUnits];
@@ -103,7 +105,18 @@ struct HostSplits {
   int32_t n;
   DenseSplit s[kHostUnits / 2];
 };
-struct NoHostUnits {};
+struct NoUnits {};
+// Paged batches of so few units that they fit the GPU at once: every CTA works out
+// its own from the lengths on the device (direct_plan), with no planning kernel
+// in front.
+struct DirectArgs {
+  const int64_t* cu;
+  const int32_t* seq_lens;
+  int32_t B, T, table_rows, can_split;
+};
+template <int MODE>
+using ModeArgs = std::conditional_t<MODE == kHost, HostUnits,
+                                    std::conditional_t<MODE == kDirect, DirectArgs, NoUnits>>;
 
 struct Unit {
   DenseUnit d;
@@ -115,16 +128,25 @@ struct Unit {
   bool dual;
 };
 
+struct DirectUnit {
+  DenseUnit d;
+  int g;  // -1: none
+};
+
 // The r-th unit of this CTA: units come longest first, and every other round
 // runs through the CTAs backwards, so that no CTA always gets the longer ones.
-template <bool HOST, typename HU>
-__device__ __forceinline__ bool get_unit(const PrefillArgs& a, const HU& hu, int total, int r,
-                                         Unit& u) {
+template <int MODE>
+__device__ __forceinline__ bool get_unit(const PrefillArgs& a, const ModeArgs<MODE>& hu,
+                                         const DirectUnit* own, int total, int r, Unit& u) {
+  if constexpr (MODE == kDirect) {
+    u.d = own->d;
+    u.g = own->g;
+  } else {
   const unsigned c = (r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
   const unsigned x = (unsigned)r * gridDim.x + c;
   const unsigned i = x / (unsigned)a.G;
   u.g = (int)(x - i * (unsigned)a.G);
-  if constexpr (HOST) {
+  if constexpr (MODE == kHost) {
     if (x >= (unsigned)total) return false;
     u.d = hu.u[i];
   } else {
@@ -134,6 +156,7 @@ __device__ __forceinline__ bool get_unit(const PrefillArgs& a, const HU& hu, int
     if (x >= (unsigned)total) return false;
     u.d.tok0 = x0.x, u.d.ntok = x0.y, u.d.pos0 = x0.z, u.d.seq = x0.w;
     u.d.kv0 = x1.x, u.d.kv1 = x1.y, u.d.slot = x1.z, u.d.row0 = x1.w;
+  }
   }
   u.nt = u.d.kv1 - u.d.kv0;
   u.dual = u.d.ntok <= a.TT;
@@ -164,12 +187,116 @@ __device__ __forceinline__ const __nv_bfloat16* v_row(const PrefillArgs& a, cons
   return a.v + (int64_t)pg * a.page_stride + ((int64_t)(s % a.page_size) * a.G + u.g) * D;
 }
 
-template <int D, bool HOST>
+constexpr int kMinPart = 4;  // key tiles worth a part: its overhead is about three
+
+// First key tile of part k of `parts` of a unit of nt key tiles.  The last part has
+// two tiles at least, so that row tile 0, which may end a key tile before row tile
+// 1, has keys in every part.
+__host__ __device__ __forceinline__ int part_begin(int k, int parts, int len, int nt) {
+  if (k >= parts) return nt;
+  return k > 0 && k * len > nt - 2 ? nt - 2 : k * len;
+}
+
+// The plan of few units by one warp, up to 32 sequences: `f` is called by one lane
+// for each unit with its first packed row, tokens, first position, sequence, key
+// tiles, key tiles per part, parts, and the parts of the units before it.  The
+// rules are dense_plan_kernel's for units that fit `ctas` CTAs at once.
+template <typename F>
+__device__ __forceinline__ void direct_plan(const DirectArgs& p, int G, int TT, int ctas,
+                                            uint32_t* err, F&& f) {
+  const int lane = lane_id(), U = 2 * TT;
+  int64_t lo = 0, hi = 0;
+  int L = 0;
+  if (lane < p.B) {
+    lo = __ldg(p.cu + lane);
+    hi = __ldg(p.cu + lane + 1);
+    L = __ldg(p.seq_lens + lane);
+  }
+  int n = (int)(hi - lo), pos = L - n;
+  if (lane < p.B && (lo < 0 || hi < lo || hi > p.T || (n > 0 && (pos < 0 || L > p.table_rows)))) {
+    record_error(err, kDevBadIndex);
+    n = 0;
+  }
+  const int units = (n + U - 1) / U;
+  int incl = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  // offsets that overlap could make more units than the host counted
+  const int total = min(__shfl_sync(0xffffffffu, incl, 31), kDirectUnits);
+  // unit 32 k + lane: its sequence and offset, and its weight (see weight below)
+  struct Own {
+    int seq, off, nt, w;
+  } own[kDirectUnits / 32];
+  int sum = 0, longest = 0;
+#pragma unroll
+  for (int k = 0; k < kDirectUnits / 32; ++k) {
+    own[k].w = 0;
+    if (32 * k >= total) continue;
+    const int x = 32 * k + lane;
+    int s = 0;
+    for (int b = 0; b < p.B; ++b) s += __shfl_sync(0xffffffffu, incl, b) <= x;
+    s = min(s, 31);
+    const int off = (x - (__shfl_sync(0xffffffffu, incl, s) - __shfl_sync(0xffffffffu, units, s))) * U;
+    const int len = __shfl_sync(0xffffffffu, n, s), p0 = __shfl_sync(0xffffffffu, pos, s);
+    if (x < total) {
+      own[k].seq = s;
+      own[k].off = off;
+      own[k].nt = (p0 + min(len, off + U) - 1) / kKeys + 1;
+      own[k].w = len - off <= TT ? (own[k].nt + 1) / 2 : own[k].nt;
+      sum += own[k].w;
+      longest = max(longest, own[k].w);
+    }
+  }
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  int part = 1 << 30;
+  if (p.can_split) {
+    for (int c = max(kMinPart, (sum * G + ctas - 1) / ctas); c < longest; ++c) {
+      int m = 0;
+#pragma unroll
+      for (int k = 0; k < kDirectUnits / 32; ++k) m += (own[k].w + c - 1) / c;
+      if (__reduce_add_sync(0xffffffffu, m) * G <= ctas) {
+        part = c;
+        break;
+      }
+    }
+  }
+  int pre = 0;
+#pragma unroll
+  for (int k = 0; k < kDirectUnits / 32; ++k) {
+    if (32 * k >= total) continue;
+    const bool mine = 32 * k + lane < total;
+    int parts = 0, len = 1;
+    if (mine) {
+      const int q = own[k].w > part ? (own[k].w + part - 1) / part : 1;
+      len = (own[k].nt + q - 1) / q;
+      parts = (own[k].nt + len - 1) / len;
+    }
+    int x = parts;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const int s = mine ? own[k].seq : 0;
+    const int64_t a = __shfl_sync(0xffffffffu, (long long)lo, s);
+    const int p0 = __shfl_sync(0xffffffffu, pos, s), ln = __shfl_sync(0xffffffffu, n, s);
+    if (mine)
+      f(a + own[k].off, min(U, ln - own[k].off), p0 + own[k].off, s, own[k].nt, len, parts,
+        pre + x - parts);
+    pre += __shfl_sync(0xffffffffu, x, 31);
+  }
+}
+
+template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v, const PrefillArgs a,
-                         const __grid_constant__ std::conditional_t<HOST, HostUnits, NoHostUnits> hu) {
+                         const __grid_constant__ ModeArgs<MODE> hu) {
   using Cfg = PrefillCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -190,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t bar_drain[2];
   __shared__ uint64_t bar_half_done, bar_half_read;  // dual units: tile 1's result, and its reading
   __shared__ float half_m[kRows], half_l[kRows];
+  __shared__ DirectUnit own_s;
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
   __shared__ int odd_v[kFlagSlots];  // an infinity or NaN was taken out of the unit's V
@@ -222,12 +350,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kFlagSlots; ++i) odd_v[i] = 0;
     fence_mbar_init();
     // nothing else clears it without a plan, and no wait runs out before this
-    if (HOST && blockIdx.x == 0 && a.clear_err) *a.err = 0;
+    if (MODE == kHost && blockIdx.x == 0 && a.clear_err) *a.err = 0;
   }
   if (threadIdx.x == 32) {
     tma_prefetch_desc(&map_q);
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
+    own_s.g = -1;
+  }
+  if constexpr (MODE == kDirect) {
+    if (warp == 1) {
+      __syncwarp();
+      const int i = blockIdx.x / a.G;
+      direct_plan(hu, a.G, a.TT, gridDim.x, a.err,
+                  [&](int64_t tok0, int ntok, int pos0, int seq, int nt, int len, int parts, int pre) {
+                    if (i < pre || i >= pre + parts) return;
+                    const int k = i - pre;
+                    own_s.d = DenseUnit{(int)tok0, ntok, pos0, seq, part_begin(k, parts, len, nt),
+                                        part_begin(k + 1, parts, len, nt),
+                                        parts > 1 ? i * a.G : -1, 0};
+                    own_s.g = blockIdx.x - i * a.G;
+                  });
+    }
   }
   if (warp == 0) {
     tmem_alloc(&tmem_base_s, 512);
@@ -240,18 +384,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &abort_s;
   pdl_launch_dependents();
   int total;
-  if constexpr (HOST) {
+  if constexpr (MODE == kHost) {
     total = hu.n * a.G;
+  } else if constexpr (MODE == kDirect) {
+    total = own_s.g >= 0 ? 1 : 0;
   } else {
     pdl_wait();  // for the units
     total = __ldcg(a.n_units) * a.G;
   }
-  const int rounds = n_rounds(total);
+  const int rounds = MODE == kDirect ? total : n_rounds(total);
 
   if (warp >= 8) {
     regs_decrease<kRegOther>();
     if (warp == kLoadWarp || warp == kLoadVWarp) {
-      // ---------------- TMA loads: Q and K, or V ----------------
+      // ---------------- TMA loads: K, or Q and V ----------------
       const bool is_v = warp == kLoadVWarp;
       const CUtensorMap* map = is_v ? &map_v : &map_k;
       const uint32_t slots = is_v ? VS : KS;
@@ -265,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       const int box_rows = a.box_rows, boxes = kKeys / box_rows;  // a lane per box of a tile
       auto load_q = [&](const Unit& u, int i) {
-        if (!ok || is_v || (i == 0 ? u.c0 : u.c1) == 0) return;
+        if (!ok || !is_v || (i == 0 ? u.c0 : u.c1) == 0) return;
         if (lane == 0) {
           ok = mbar_wait(&bar_q_empty[i], (qn[i] & 1) ^ 1, abort_flag, a.err, kDevTimeoutMma);
           if (ok) {
@@ -281,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int r = 0; r < rounds && ok; ++r) {
         Unit u;
-        if (!get_unit<HOST>(a, hu, total, r, u)) continue;
+        if (!get_unit<MODE>(a, hu, &own_s, total, r, u)) continue;
         const int keys_end = u.d.pos0 + u.d.ntok;
         const int part0 = first_partial(u) - u.d.kv0;
         // lane i: page of box i of a key tile (0: none, or packed rows)
@@ -306,7 +452,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               page = a.num_pages;  // outside the tensor: reads zeros
             }
           }
-          if (j == 0) load_q(u, 0);
+          if (j == 0) {
+            load_q(u, 0);
+            load_q(u, 1);
+          }
           if (!ok) break;
           uint64_t* full;
           uint32_t par;
@@ -336,7 +485,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           if (++slot == slots) slot = 0, phase ^= 1;
-          if (j == 0) load_q(u, 1);
         }
       }
       if (lane == 0 && *abort_flag) {
@@ -373,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t slot = 0, phase = 0;  // of the K tile
         for (int r = 0; r < rounds && ok; ++r) {
           Unit u;
-          if (!get_unit<HOST>(a, hu, total, r, u)) continue;
+          if (!get_unit<MODE>(a, hu, &own_s, total, r, u)) continue;
           // broadcasts: known to be the same in every lane
           const int cnt[2] = {__shfl_sync(0xffffffffu, u.c0, 0), __shfl_sync(0xffffffffu, u.c1, 0)};
           const bool dual = __shfl_sync(0xffffffffu, (int)u.dual, 0) != 0;
@@ -418,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t slot = 0;  // of the V tile
         for (int r = 0; r < rounds && ok; ++r) {
           Unit u;
-          if (!get_unit<HOST>(a, hu, total, r, u)) continue;
+          if (!get_unit<MODE>(a, hu, &own_s, total, r, u)) continue;
           const int cnt[2] = {__shfl_sync(0xffffffffu, u.c0, 0), __shfl_sync(0xffffffffu, u.c1, 0)};
           const int part0 = __shfl_sync(0xffffffffu, first_partial(u) - u.d.kv0, 0);
           const bool dual = __shfl_sync(0xffffffffu, (int)u.dual, 0) != 0;
@@ -522,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int r = 0; r < rounds && ok; ++r) {
       Unit u;
-      if (!get_unit<HOST>(a, hu, total, r, u)) continue;
+      if (!get_unit<MODE>(a, hu, &own_s, total, r, u)) continue;
       base += prev_nt;
       cleaned += prev_special;
       const int part0 = first_partial(u) - u.d.kv0;
@@ -764,20 +912,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;  // at most
 constexpr int kBuckets = 256;
-constexpr int kMinPart = 4;  // key tiles worth a part: its overhead is about three
 
 __device__ __forceinline__ int bucket_of(int tiles) {  // longer first; tiles >= 1
   const int e = 31 - __clz(tiles);
   const int f = e >= 3 ? (tiles >> (e - 3)) & 7 : (tiles << (3 - e)) & 7;
   return kBuckets - 1 - (e * 8 + f);
-}
-
-// First key tile of part k of `parts` of a unit of nt key tiles.  The last part has
-// two tiles at least, so that row tile 0, which may end a key tile before row tile
-// 1, has keys in every part.
-__host__ __device__ __forceinline__ int part_begin(int k, int parts, int len, int nt) {
-  if (k >= parts) return nt;
-  return k > 0 && k * len > nt - 2 ? nt - 2 : k * len;
 }
 
 struct PlanArgs {
@@ -948,18 +1087,38 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // out = sum_z 2^(m_z - M) O_z / sum_z 2^(m_z - M) l_z over the partials z of every
 // split unit; a warp per row, D/32 columns a lane.
-template <int D, bool HOST>
+template <int D, int MODE>
 __global__ void __launch_bounds__(256)
-    dense_combine_kernel(const __grid_constant__ std::conditional_t<HOST, HostSplits, NoHostUnits> hs,
+    dense_combine_kernel(const __grid_constant__ std::conditional_t<
+                             MODE == kHost, HostSplits,
+                             std::conditional_t<MODE == kDirect, DirectArgs, NoUnits>> hs,
                          const DenseSplit* splits, const int32_t* counts, const float* part_o,
-                         const float2* part_ml, int H, int G, int TT, __nv_bfloat16* out) {
-  pdl_wait();
+                         const float2* part_ml, int H, int G, int TT, int ctas,
+                         __nv_bfloat16* out) {
   const int HG = H / G;
   int n;
-  if constexpr (HOST)
+  if constexpr (MODE == kDirect) {
+    __shared__ DenseSplit table[kDirectUnits];
+    __shared__ int n_s;
+    splits = table;
+    if (threadIdx.x == 0) n_s = 0;
+    __syncthreads();
+    if (warp_id() == 0)
+      direct_plan(hs, G, TT, ctas, nullptr,
+                  [&](int64_t tok0, int ntok, int, int, int, int, int parts, int pre) {
+                    if (parts > 1)
+                      table[atomicAdd(&n_s, 1)] = DenseSplit{(int)tok0, ntok, pre * G, parts};
+                  });
+    __syncthreads();
+    n = n_s;
+    pdl_wait();
+  } else if constexpr (MODE == kHost) {
+    pdl_wait();
     n = hs.n;
-  else
+  } else {
+    pdl_wait();
     n = __ldcg(counts + 1);
+  }
   const int per_tile = TT * HG, per_unit = 2 * per_tile;  // rows
   const unsigned rows = (unsigned)n * G * per_unit;       // at most (CTAs / 2) * 256
   const int lane = lane_id();
@@ -969,9 +1128,13 @@ __global__ void __launch_bounds__(256)
     const int urow = (int)(x - y * per_unit);
     const int g = (int)(y % G);
     int4 sp;
-    if constexpr (HOST) {
-      const DenseSplit& d = hs.s[y / G];
-      sp = make_int4(d.tok0, d.ntok, d.slot, d.parts);
+    if constexpr (MODE != kPlanned) {
+      const DenseSplit* d;
+      if constexpr (MODE == kHost)
+        d = hs.s + y / G;
+      else
+        d = splits + y / G;
+      sp = make_int4(d->tok0, d->ntok, d->slot, d->parts);
     } else {
       sp = __ldcg(reinterpret_cast<const int4*>(splits + y / G));
     }
@@ -1191,16 +1354,43 @@ cudaError_t launch_impl(const DensePrefillLaunch& p, cudaStream_t s, int* launch
   HostSplits hs;
   cudaError_t e;
   if (!p.cu && host_plan(p, TT, hu, hs)) {
-    auto kern = dense_prefill_kernel<D, true>;
+    auto kern = dense_prefill_kernel<D, kHost>;
     if ((e = prepare(kern, Cfg::kSmem)) != cudaSuccess) return e;
     const int grid = (int)min64((int64_t)hu.n * p.G, p.grid);
     kern<<<grid, kThreads, Cfg::kSmem, s>>>(mq, mk, mv, a, hu);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ++*launches;
     if (hs.n > 0) {
-      e = launch_early(dense_combine_kernel<D, true>, combine_grid, 256, 0, s, hs,
+      e = launch_early(dense_combine_kernel<D, kHost>, combine_grid, 256, 0, s, hs,
                        (const DenseSplit*)nullptr, (const int32_t*)nullptr, (const float*)p.part_o,
-                       (const float2*)p.part_ml, p.H, p.G, TT, a.out);
+                       (const float2*)p.part_ml, p.H, p.G, TT, p.grid, a.out);
+      if (e != cudaSuccess) return e;
+      ++*launches;
+    }
+    return cudaSuccess;
+  }
+
+  const int table_rows = paged ? (int)min64((int64_t)p.cache.table_stride * p.cache.page_size,
+                                            (int64_t)1 << 30)
+                               : 0;
+  if (p.cu && p.B <= 32 && (p.T / (2 * TT) + p.B) * p.G <= min64(p.grid, kDirectUnits)) {
+    if ((e = cudaMemsetAsync(p.err, 0, sizeof(uint32_t), s)) != cudaSuccess) return e;
+    DirectArgs da;
+    da.cu = p.cu;
+    da.seq_lens = p.seq_lens;
+    da.B = p.B;
+    da.T = (int32_t)p.T;
+    da.table_rows = table_rows;
+    da.can_split = p.max_slots > 0;
+    auto kern = dense_prefill_kernel<D, kDirect>;
+    if ((e = prepare(kern, Cfg::kSmem)) != cudaSuccess) return e;
+    kern<<<p.grid, kThreads, Cfg::kSmem, s>>>(mq, mk, mv, a, da);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    ++*launches;
+    if (p.max_slots > 0) {
+      e = launch_early(dense_combine_kernel<D, kDirect>, combine_grid, 256, 0, s, da,
+                       (const DenseSplit*)nullptr, (const int32_t*)nullptr, (const float*)p.part_o,
+                       (const float2*)p.part_ml, p.H, p.G, TT, p.grid, a.out);
       if (e != cudaSuccess) return e;
       ++*launches;
     }
@@ -1214,9 +1404,7 @@ cudaError_t launch_impl(const DensePrefillLaunch& p, cudaStream_t s, int* launch
   pl.T = (int32_t)p.T;
   pl.G = p.G;
   pl.TT = TT;
-  pl.table_rows = paged ? (int32_t)min64((int64_t)p.cache.table_stride * p.cache.page_size,
-                                         (int64_t)1 << 30)
-                        : 0;
+  pl.table_rows = table_rows;
   pl.ctas = p.grid;
   pl.can_split = p.max_slots > 0;
   pl.max_units = p.max_units;
@@ -1230,15 +1418,15 @@ cudaError_t launch_impl(const DensePrefillLaunch& p, cudaStream_t s, int* launch
   dense_plan_kernel<<<1, plan_threads, 0, s>>>(*p.offsets, pl);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   ++*launches;
-  auto kern = dense_prefill_kernel<D, false>;
+  auto kern = dense_prefill_kernel<D, kPlanned>;
   if ((e = prepare(kern, Cfg::kSmem)) != cudaSuccess) return e;
-  e = launch_early(kern, p.grid, kThreads, Cfg::kSmem, s, mq, mk, mv, a, NoHostUnits{});
+  e = launch_early(kern, p.grid, kThreads, Cfg::kSmem, s, mq, mk, mv, a, NoUnits{});
   if (e != cudaSuccess) return e;
   ++*launches;
   if (p.max_slots > 0) {
-    e = launch_early(dense_combine_kernel<D, false>, combine_grid, 256, 0, s, NoHostUnits{},
+    e = launch_early(dense_combine_kernel<D, kPlanned>, combine_grid, 256, 0, s, NoUnits{},
                      (const DenseSplit*)p.splits, (const int32_t*)p.counts, (const float*)p.part_o,
-                     (const float2*)p.part_ml, p.H, p.G, TT, a.out);
+                     (const float2*)p.part_ml, p.H, p.G, TT, p.grid, a.out);
     if (e != cudaSuccess) return e;
     ++*launches;
   }

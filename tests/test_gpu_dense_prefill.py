@@ -122,6 +122,22 @@ def test_paged_few_rows_over_long_caches_are_split(msa):
     run_paged(msa, 16, 2, 64, 64, [1], [9001])
 
 
+@pytest.mark.parametrize("H,G,d", [(8, 2, 64), (5, 1, 128)])
+def test_paged_many_sequences_are_planned_on_the_device(msa, H, G, d):
+    """More than 32 sequences: a planning kernel, units longest first, a long one split."""
+    rng = np.random.default_rng(11)
+    new = rng.integers(0, 12, size=45).tolist()
+    ctx = rng.integers(0, 200, size=45).tolist()
+    new[7], ctx[7] = 70, 9000
+    new[40], ctx[40] = 300, 11
+    run_paged(msa, H, G, d, 32, new, ctx, pad=3)
+
+
+def test_paged_many_units_are_planned_on_the_device(msa):
+    """More units than CTAs: several per CTA, none split."""
+    run_paged(msa, 8, 8, 64, 128, [2600, 2100], [30, 0])
+
+
 def test_paged_padded_batch_and_strided_pages(msa):
     run_paged(msa, 4, 2, 64, 32, [5, 9], [100, 0], pad=7, side_by_side=True, table_cols=11)
 
