@@ -30,7 +30,7 @@
 // Warp roles (384 threads, one CTA per SM, persistent over the units):
 //   WG0, WG1  softmax of row tile 0 / 1, one thread per row; the rescaling of
 //             O; the cleaning of V; the final O / l;
-//   WG2       warp 8 loads K, warp 11 Q and V (TMA; with pages of 16 tokens a
+//   WG2       warp 8 loads Q and K, warp 11 V (TMA; with pages of 16 tokens a
 //             tile of 128 keys is 16 copies), warp 9 issues S, warp 10 issues PV.
 // TMEM (512 columns): one S buffer for both row tiles (0-127), P0, P1 (64 columns
 // each) and O0, O1.  A softmax thread copies its row of S into registers at once,
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 8) {
     regs_decrease<kRegOther>();
     if (warp == kLoadWarp || warp == kLoadVWarp) {
-      // ---------------- TMA loads: K, or Q and V ----------------
+      // ---------------- TMA loads: Q and K, or V ----------------
       const bool is_v = warp == kLoadVWarp;
       const CUtensorMap* map = is_v ? &map_v : &map_k;
       const uint32_t slots = is_v ? VS : KS;
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       const int box_rows = a.box_rows, boxes = kKeys / box_rows;  // a lane per box of a tile
       auto load_q = [&](const Unit& u, int i) {
-        if (!ok || !is_v || (i == 0 ? u.c0 : u.c1) == 0) return;
+        if (!ok || is_v || (i == 0 ? u.c0 : u.c1) == 0) return;
         if (lane == 0) {
           ok = mbar_wait(&bar_q_empty[i], (qn[i] & 1) ^ 1, abort_flag, a.err, kDevTimeoutMma);
           if (ok) {
@@ -452,10 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               page = a.num_pages;  // outside the tensor: reads zeros
             }
           }
-          if (j == 0) {
-            load_q(u, 0);
-            load_q(u, 1);
-          }
+          if (j == 0) load_q(u, 0);
           if (!ok) break;
           uint64_t* full;
           uint32_t par;
@@ -485,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           if (++slot == slots) slot = 0, phase ^= 1;
+          if (j == 0) load_q(u, 1);
         }
       }
       if (lane == 0 && *abort_flag) {

@@ -9,11 +9,10 @@
 // off by 0.06); sine and cosine of the fraction, the rotation and nothing else
 // are fp32, rounded once to bf16.
 //
-// Memory bound: every element is read and written once.  A thread owns the same
-// 16 dimensions of a head (two 16-byte pieces that hold 8 whole pairs in either
-// layout) in every head it visits, so a token's 8 sines and cosines are read
-// from shared memory once per thread, not once per head; a token's angles are
-// computed once per CTA.
+// Memory bound: every element is read and written once.  A CTA takes a few tokens:
+// their rows in the cache and their sines and cosines first, then 16 dimensions of
+// a head per thread and turn (two 16-byte pieces that hold 8 whole pairs in either
+// layout).  A 32K prompt of 64 + 2 x 8 heads of 128 moves at 5.8 TB/s.
 #include "kernels.h"
 #include "sm100.cuh"
 
@@ -52,46 +51,68 @@ struct Args {
   uint32_t* err;
 };
 
-// D: head size; IL: adjacent pairs; TOK: tokens per CTA.
-template <int D, bool IL, int TOK>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const Args a) {
-  constexpr int kItems = D / 16;               // 16-dimension items of a head
-  constexpr int kHeadLanes = kThreads / kItems;  // heads visited at once
-  __shared__ float2 cs[TOK][D / 2];  // (cos, sin)
-  __shared__ int64_t kv_off[TOK];    // element offset of the token's row in the cache, -1: none
-  __shared__ int64_t pos_s[TOK];     // -1: not a token of any sequence
+// Where token t's row is: its position (-1: of no sequence, or of an invalid one)
+// and the element offset in the cache (-1: none).  A whole warp.
+__device__ __forceinline__ void locate(const Args& a, int64_t t, int row_elems, int64_t& pos,
+                                       int64_t& off) {
+  pos = off = -1;
+  if (t >= a.T) return;
+  const int lane = lane_id();
+  int b;
+  int64_t begin, end;
+  int L;
+  if (a.B < 32) {  // all offsets and lengths in one round trip
+    const int64_t c = lane <= a.B ? __ldg(a.cu + lane) : 0;
+    const int l = lane < a.B ? __ldg(a.seq_lens + lane) : 0;
+    const unsigned m = __ballot_sync(0xffffffffu, lane < a.B && c <= t);
+    if (m == 0) return;
+    b = 31 - __clz(m);
+    begin = __shfl_sync(0xffffffffu, c, b);
+    end = __shfl_sync(0xffffffffu, c, b + 1);
+    L = __shfl_sync(0xffffffffu, l, b);
+    if (t >= __shfl_sync(0xffffffffu, c, a.B)) return;
+  } else {
+    if (t < __ldg(a.cu) || t >= __ldg(a.cu + a.B)) return;
+    b = find_seq(a.cu, a.B, t);
+    begin = __ldg(a.cu + b);
+    end = __ldg(a.cu + b + 1);
+    L = __ldg(a.seq_lens + b);
+  }
+  const int64_t p = (int64_t)L - (end - t);
+  // offsets that are not ascending, a sequence with fewer keys than new tokens,
+  // or a row past the block table
+  if (t < begin || t >= end || p < t - begin ||
+      p >= (int64_t)a.cache.table_stride * a.cache.page_size) {
+    if (lane == 0) record_error(a.err, kDevBadIndex);
+    return;
+  }
+  pos = p;
+  const int pg = __ldg(a.cache.block_table + (int64_t)b * a.cache.table_stride + p / a.cache.page_size);
+  if (pg < 0 || pg >= a.cache.num_pages) {
+    if (lane == 0) record_error(a.err, kDevBadIndex);
+    return;
+  }
+  off = (int64_t)pg * a.cache.page_stride + (p % a.cache.page_size) * (int64_t)row_elems;
+}
+
+constexpr int kMaxTok = 16;
+
+// D: head size; IL: adjacent pairs; tok: tokens per CTA.
+template <int D, bool IL>
+__global__ void __launch_bounds__(kThreads) rope_append_kernel(const Args a, const int tok) {
+  constexpr int kItems = D / 16;     // 16-dimension items of a head
+  __shared__ float2 cs[kMaxTok][D / 2];  // (cos, sin)
+  __shared__ int64_t off_s[kMaxTok], pos_s[kMaxTok];
   const int tid = threadIdx.x;
-  const int64_t t0 = (int64_t)blockIdx.x * TOK;
-  for (int i = warp_id(); i < TOK; i += kThreads / 32) {
-    const int64_t t = t0 + i;
-    int64_t pos = -1, off = -1;
-    if (t < a.T && t >= __ldg(a.cu) && t < __ldg(a.cu + a.B)) {
-      const int b = find_seq(a.cu, a.B, t);
-      const int64_t end = __ldg(a.cu + b + 1);
-      pos = (int64_t)__ldg(a.seq_lens + b) - (end - t);
-      // a sequence with fewer keys than new tokens, offsets that are not
-      // ascending, or a row past the block table
-      if (t < __ldg(a.cu + b) || t >= end ||
-          pos < t - __ldg(a.cu + b) ||
-          pos >= (int64_t)a.cache.table_stride * a.cache.page_size) {
-        if (lane_id() == 0) record_error(a.err, kDevBadIndex);
-        pos = -1;
-      } else {
-        const int pg = __ldg(a.cache.block_table + (int64_t)b * a.cache.table_stride +
-                             pos / a.cache.page_size);
-        if (pg < 0 || pg >= a.cache.num_pages) {
-          if (lane_id() == 0) record_error(a.err, kDevBadIndex);
-        } else {
-          off = (int64_t)pg * a.cache.page_stride +
-                (pos % a.cache.page_size) * (int64_t)a.G * D;
-        }
-      }
-    }
-    if (lane_id() == 0) pos_s[i] = pos, kv_off[i] = off;
+  const int64_t t0 = (int64_t)blockIdx.x * tok;
+  for (int i = warp_id(); i < tok; i += kThreads / 32) {
+    int64_t pos, off;
+    locate(a, t0 + i, a.G * D, pos, off);
+    if (lane_id() == 0) pos_s[i] = pos, off_s[i] = off;
   }
   __syncthreads();
   const int nf = a.rot / 2;
-  for (int x = tid; x < TOK * nf; x += kThreads) {
+  for (int x = tid; x < tok * nf; x += kThreads) {
     const int i = x / nf, j = x - i * nf;
     const int64_t pos = pos_s[i];
     if (pos < 0) continue;
@@ -104,90 +125,70 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const Args a) {
   }
   __syncthreads();
 
-  const int item = tid % kItems, hl = tid / kItems;
-  const bool rotated = item * 16 < a.rot;
-  // the two 16-byte pieces of the item
-  int c0, c1;
-  if (IL || !rotated) {
-    c0 = item * 2;
-    c1 = c0 + 1;
-  } else {
-    c0 = item;
-    c1 = item + a.rot / 16;
-  }
-  const int heads = (a.q ? a.H : 0) + a.G;  // rotated heads; the values follow
-#pragma unroll 1
-  for (int i = 0; i < TOK; ++i) {
-    if (pos_s[i] < 0) continue;
-    const int64_t t = t0 + i;
-    float cc[8], ss[8];
-    if (rotated) {
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float4 w = *reinterpret_cast<const float4*>(&cs[i][item * 8 + e]);
-        cc[e] = w.x, ss[e] = w.y, cc[e + 1] = w.z, ss[e + 1] = w.w;
-      }
+  const int nq = a.q ? a.H : 0, nr = nq + a.G, heads = nr + a.G;  // queries, keys; then values
+  const int per_tok = heads * kItems, total = tok * per_tok;
+#pragma unroll 4
+  for (int x = tid; x < total; x += kThreads) {
+    const int i = x / per_tok, y = x - i * per_tok;
+    const int h = y / kItems, item = y % kItems;
+    const int64_t t = t0 + i, off = off_s[i];
+    if (pos_s[i] < 0 || (h >= nq && off < 0)) continue;
+    const bool rotated = h < nr && item * 16 < a.rot;
+    // the two 16-byte pieces of the item
+    int c0 = item * 2, c1 = item * 2 + 1;
+    if (!IL && item * 16 < a.rot) c0 = item, c1 = item + a.rot / 16;
+    const uint8_t* src;
+    uint8_t* dst;
+    if (h < nq) {
+      src = a.q + t * a.q_stride + h * (D * 2);
+      dst = a.q_out + (t * a.H + h) * (int64_t)(D * 2);
+    } else if (h < nr) {
+      src = a.k + t * a.k_stride + (h - nq) * (D * 2);
+      dst = static_cast<uint8_t*>(a.cache.k) + (off + (h - nq) * D) * 2;
+    } else {
+      src = a.v + t * a.v_stride + (h - nr) * (D * 2);
+      dst = static_cast<uint8_t*>(a.cache.v) + (off + (h - nr) * D) * 2;
     }
-    const int64_t off = kv_off[i];
-    const uint8_t* qrow = a.q + t * a.q_stride;
-    const uint8_t* krow = a.k + t * a.k_stride;
-    const uint8_t* vrow = a.v + t * a.v_stride;
-    const int nq = heads - a.G;
-    const int end = off >= 0 ? heads + a.G : nq;  // a token without a row in the cache: q only
-#pragma unroll 3
-    for (int h = hl; h < end; h += kHeadLanes) {
-      const uint8_t* src;
-      uint8_t* dst;
-      if (h < nq) {
-        src = qrow + (int64_t)h * D * 2;
-        dst = a.q_out + (t * a.H + h) * (int64_t)D * 2;
-      } else if (h < heads) {
-        src = krow + (int64_t)(h - nq) * D * 2;
-        dst = static_cast<uint8_t*>(a.cache.k) + (off + (int64_t)(h - nq) * D) * 2;
-      } else {
-        src = vrow + (int64_t)(h - heads) * D * 2;
-        dst = static_cast<uint8_t*>(a.cache.v) + (off + (int64_t)(h - heads) * D) * 2;
-      }
-      uint4 x = *reinterpret_cast<const uint4*>(src + c0 * 16);
-      uint4 y = *reinterpret_cast<const uint4*>(src + c1 * 16);
-      if (rotated && h < heads) {
-        uint32_t *xw = &x.x, *yw = &y.x;
+    uint4 u = *reinterpret_cast<const uint4*>(src + c0 * 16);
+    uint4 w = *reinterpret_cast<const uint4*>(src + c1 * 16);
+    if (rotated) {
+      uint32_t *uw = &u.x, *ww = &w.x;
+      const float4* tr = reinterpret_cast<const float4*>(&cs[i][item * 8]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 r = tr[e];  // cos, sin of pairs 2e and 2e + 1
         if (IL) {
           // a word holds one pair
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            uint32_t& w = e < 4 ? xw[e] : yw[e - 4];
-            const float p = __uint_as_float(w << 16), q = __uint_as_float(w & 0xFFFF0000u);
-            w = pack_bf16x2(p * cc[e] - q * ss[e], q * cc[e] + p * ss[e]);
-          }
+          uint32_t& w0 = e < 2 ? uw[2 * e] : ww[2 * e - 4];
+          uint32_t& w1 = e < 2 ? uw[2 * e + 1] : ww[2 * e - 3];
+          const float p0 = __uint_as_float(w0 << 16), q0 = __uint_as_float(w0 & 0xFFFF0000u);
+          const float p1 = __uint_as_float(w1 << 16), q1 = __uint_as_float(w1 & 0xFFFF0000u);
+          w0 = pack_bf16x2(p0 * r.x - q0 * r.y, q0 * r.x + p0 * r.y);
+          w1 = pack_bf16x2(p1 * r.z - q1 * r.w, q1 * r.z + p1 * r.w);
         } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float p0 = __uint_as_float(xw[e] << 16);
-            const float p1 = __uint_as_float(xw[e] & 0xFFFF0000u);
-            const float q0 = __uint_as_float(yw[e] << 16);
-            const float q1 = __uint_as_float(yw[e] & 0xFFFF0000u);
-            const float c_0 = cc[2 * e], s_0 = ss[2 * e], c_1 = cc[2 * e + 1], s_1 = ss[2 * e + 1];
-            xw[e] = pack_bf16x2(p0 * c_0 - q0 * s_0, p1 * c_1 - q1 * s_1);
-            yw[e] = pack_bf16x2(q0 * c_0 + p0 * s_0, q1 * c_1 + p1 * s_1);
-          }
+          const float p0 = __uint_as_float(uw[e] << 16), p1 = __uint_as_float(uw[e] & 0xFFFF0000u);
+          const float q0 = __uint_as_float(ww[e] << 16), q1 = __uint_as_float(ww[e] & 0xFFFF0000u);
+          uw[e] = pack_bf16x2(p0 * r.x - q0 * r.y, p1 * r.z - q1 * r.w);
+          ww[e] = pack_bf16x2(q0 * r.x + p0 * r.y, q1 * r.z + p1 * r.w);
         }
       }
-      *reinterpret_cast<uint4*>(dst + c0 * 16) = x;
-      *reinterpret_cast<uint4*>(dst + c1 * 16) = y;
     }
+    *reinterpret_cast<uint4*>(dst + c0 * 16) = u;
+    *reinterpret_cast<uint4*>(dst + c1 * 16) = w;
   }
 }
 
 template <int D, bool IL>
 cudaError_t launch_d(const RopeAppendLaunch& p, const Args& a, cudaStream_t s) {
-  // one token per CTA while that leaves CTAs idle, four otherwise
-  constexpr int kTok = 4;
-  if (p.T <= (int64_t)p.num_sms * 8) {
-    rope_append_kernel<D, IL, 1><<<(unsigned)p.T, kThreads, 0, s>>>(a);
-  } else {
-    rope_append_kernel<D, IL, kTok><<<(unsigned)((p.T + kTok - 1) / kTok), kThreads, 0, s>>>(a);
-  }
+  // Items per CTA: ten a thread where that still makes eight CTAs per SM, which
+  // spreads a token's sequence search and angles over more bytes; else two or
+  // three, for more CTAs at once.
+  const int64_t per_tok = (int64_t)((p.q ? p.H : 0) + 2 * p.G) * (D / 16);
+  const int64_t want = p.T * per_tok >= (int64_t)p.num_sms * 8 * 10 * kThreads ? 10 * kThreads
+                                                                              : 5 * kThreads / 2;
+  int tok = 1;
+  while (tok < kMaxTok && 2 * tok * per_tok <= want) tok *= 2;
+  rope_append_kernel<D, IL><<<(unsigned)((p.T + tok - 1) / tok), kThreads, 0, s>>>(a, tok);
   return cudaGetLastError();
 }
 
