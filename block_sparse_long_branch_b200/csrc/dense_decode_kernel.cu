@@ -281,19 +281,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s = issued % Cfg::kStages;
     const int key0 = (ld.st + ki + ld_k * kw) * kStep;
     const int n = min(boxes, (ld.L - key0 + box_rows - 1) / box_rows);
-    int pg = __shfl_sync(0xffffffffu, pages, ld_k % ahead * boxes + lane % boxes);
-    if (lane == 0) mbar_arrive_expect_tx(&bar_full[warp][s], n * box_rows * D * 4);
-    __syncwarp();
-    if (lane < n) {
+    // copies with operands known to be the same in the whole warp (see elect_one)
+    const int g = (ld.bd * gw + gi) / a.HC;
+    uint64_t* bar = &bar_full[warp][s];
+    uint8_t* dst = ring + s * Cfg::kStageBytes;
+    if (elect_one()) mbar_arrive_expect_tx(bar, n * box_rows * D * 4);
+    for (int b = 0; b < n; ++b, dst += box_rows * 128) {
+      int pg = __shfl_sync(0xffffffffu, pages, ld_k % ahead * boxes + b);
       if (pg < 0 || pg >= a.num_pages) {
         record_error(a.err, kDevBadIndex);
         pg = a.num_pages;  // outside the tensor: reads zeros
       }
-      const int row = (key0 + lane * box_rows) % a.page_size;
-      const int g = (ld.bd * gw + gi) / a.HC;
-      uint8_t* dst = ring + s * Cfg::kStageBytes + lane * box_rows * 128;
-      tma_load_5d(dst, &map_k, &bar_full[warp][s], 0, row, 0, g, pg);
-      tma_load_5d(dst + Cfg::kHalf, &map_v, &bar_full[warp][s], 0, row, 0, g, pg);
+      const int row = (key0 + b * box_rows) % a.page_size;
+      if (elect_one()) {
+        tma_load_5d(dst, &map_k, bar, 0, row, 0, g, pg);
+        tma_load_5d(dst + Cfg::kHalf, &map_v, bar, 0, row, 0, g, pg);
+      }
     }
     __syncwarp();
     ++issued;

@@ -412,17 +412,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int box_rows = a.box_rows, boxes = kKeys / box_rows;  // a lane per box of a tile
       auto load_q = [&](const Unit& u, int i) {
         if (!ok || is_v || (i == 0 ? u.c0 : u.c1) == 0) return;
-        if (lane == 0) {
-          ok = mbar_wait(&bar_q_empty[i], (qn[i] & 1) ^ 1, abort_flag, a.err, kDevTimeoutMma);
-          if (ok) {
-            mbar_arrive_expect_tx(&bar_q_full[i], (uint32_t)(a.TT * a.HG * D * 2));
+        ok = __all_sync(0xffffffffu, mbar_wait(&bar_q_empty[i], (qn[i] & 1) ^ 1, abort_flag, a.err,
+                                               kDevTimeoutMma));
+        if (ok && elect_one()) {
+          mbar_arrive_expect_tx(&bar_q_full[i], (uint32_t)(a.TT * a.HG * D * 2));
 #pragma unroll
-            for (int c = 0; c < Cfg::kChunks; ++c)
-              tma_load_4d(sQ + i * Cfg::kTileBytes + c * kRows * 128, &map_q, &bar_q_full[i], 0,
-                          u.g * a.HG, c, u.d.tok0 + (u.dual ? 0 : i * a.TT));
-          }
+          for (int c = 0; c < Cfg::kChunks; ++c)
+            tma_load_4d(sQ + i * Cfg::kTileBytes + c * kRows * 128, &map_q, &bar_q_full[i], 0,
+                        u.g * a.HG, c, u.d.tok0 + (u.dual ? 0 : i * a.TT));
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        __syncwarp();
         if (ok) ++qn[i];
       };
       for (int r = 0; r < rounds && ok; ++r) {
@@ -466,19 +465,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             full = &bar_spec[special % VS];
             par = (special++ / VS) & 1;
           }
-          if (lane == 0) {
-            ok = mbar_wait(&empty[slot], phase ^ 1, abort_flag, a.err, kDevTimeoutMma);
-            if (ok) mbar_arrive_expect_tx(full, (uint32_t)(nbox * box_rows * D * 2));
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(&empty[slot], phase ^ 1, abort_flag, a.err, kDevTimeoutMma));
           if (!ok) break;
+          if (elect_one()) mbar_arrive_expect_tx(full, (uint32_t)(nbox * box_rows * D * 2));
+          __syncwarp();
           last_full = full;
           last_par = par;
-          if (lane < nbox) {
-            uint8_t* dst = ring + slot * Cfg::kTileBytes + lane * box_rows * 128;
+          // One copy after the other with operands known to be the same in the
+          // whole warp; a lane each, they are issued in a loop over the lanes.
+          uint8_t* dst = ring + slot * Cfg::kTileBytes;
+          for (int b = 0; b < nbox; ++b, dst += box_rows * 128) {
+            const int row_b = __shfl_sync(0xffffffffu, row, b);
+            const int page_b = __shfl_sync(0xffffffffu, page, b);
+            if (elect_one()) {
 #pragma unroll
-            for (int c = 0; c < Cfg::kChunks; ++c)
-              tma_load_5d(dst + c * kKeys * 128, map, full, 0, row, c, u.g, page);
+              for (int c = 0; c < Cfg::kChunks; ++c)
+                tma_load_5d(dst + c * kKeys * 128, map, full, 0, row_b, c, u.g, page_b);
+            }
           }
           __syncwarp();
           if (++slot == slots) slot = 0, phase ^= 1;
