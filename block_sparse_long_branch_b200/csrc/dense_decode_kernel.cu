@@ -98,6 +98,14 @@ __device__ __forceinline__ int n_steps(int L) {
   return (L + STEP - 1) / STEP;
 }
 
+// quotients of the line, mostly far below 2^32 (a 64-bit division is ten times slower)
+__device__ __forceinline__ long long div_down(long long x, long long y) {
+  return ((x | y) >> 32) == 0 ? (long long)((unsigned)x / (unsigned)y) : x / y;
+}
+__device__ __forceinline__ long long div_up(long long x, long long y) {
+  return div_down(x + y - 1, y);
+}
+
 // A position in the line: step `st` of bundle `bd` (gw neighbouring items) of sequence b.
 struct Cursor {
   int b, bd;
@@ -118,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   float* join = reinterpret_cast<float*>(smem + kWarps * Cfg::kStages * Cfg::kStageBytes);
   __shared__ uint64_t bar_full[kWarps][Cfg::kStages];
-  __shared__ float jm[kWarps][ROWS], jl[kWarps][ROWS];
+  __shared__ float jm[kWarps][ROWS], jl[kWarps][ROWS], jf[kWarps][ROWS];
   __shared__ long long red[kWarps];
   __shared__ long long start_off;
   __shared__ int start_b, start_len;
@@ -164,20 +172,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int b0 = 0; b0 < a.B; b0 += kThreads) {
     const int b = b0 + me;
     len = b < a.B ? seq_len(a, b) : 0;
-    if (b < a.B && len == 0 && b % (int)gridDim.x == (int)blockIdx.x && tid == me) {
-      // an empty sequence: zeros
-      uint4* o = reinterpret_cast<uint4*>(a.out + (int64_t)b * a.H * D);
-      for (int x = 0; x < a.H * D / 8; ++x) o[x] = make_uint4(0, 0, 0, 0);
-    }
     // steps below 2^40, sequences above it: one sum for both
     const long long sum = prefix((long long)n_steps<kStep>(len) + (len > 0 ? 1ll << 40 : 0), before);
     total += sum & ((1ll << 40) - 1);
     seqs += sum >> 40;
   }
+  // empty sequences: zeros
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (seq_len(a, b) > 0) continue;
+    uint4* o = reinterpret_cast<uint4*>(a.out + (int64_t)b * a.H * D);
+    for (int x = tid; x < a.H * D / 8; x += kThreads) o[x] = make_uint4(0, 0, 0, 0);
+  }
   // ---- groups at a time, and the line ----
   // gw: as many groups as divide the items evenly, while a share keeps 16 steps
+  // and a bundle spans 16 shares at most on average: its parts are joined by one
+  // CTA (one sequence of 1M, 8 groups: 745 us with all eight at a time, 660 with
+  // one; 16 of 256K and one of 1M: 3.07 ms with eight, 3.33 with two).
   int gw = (items & 7) == 0 ? 8 : (items & 3) == 0 ? 4 : (items & 1) == 0 ? 2 : 1;
-  while (gw > 1 && total * items < 16ll * gw * gridDim.x) gw >>= 1;
+  while (gw > 1 && (total * items < 16ll * gw * gridDim.x || seqs * items * 16 < (long long)gw * gridDim.x))
+    gw >>= 1;
   const int kw = kWarps / gw, bundles = items / gw;
   const int gi = warp % gw, ki = warp / gw;  // this warp's group of the bundle, and its steps' offset
   // A part costs about as much as 4 steps of each warp beside its steps (its
@@ -189,11 +202,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int cost = padded ? 0 : 4 * kw;
   const long long line = total * bundles + cost * n_bundles;
   const long long ctas = padded ? gridDim.x - n_bundles : gridDim.x;
-  long long share = (line + ctas - 1) / ctas;
+  long long share = div_up(line, ctas);
   if (share < kw) share = kw;
   auto length = [&](int n) -> long long {  // of a bundle of n steps in the line
     if (n == 0) return 0;
-    return padded ? (n + share - 1) / share * share : (long long)n + cost;
+    return padded ? div_up(n, share) * share : (long long)n + cost;
   };
   const long long lo = share * blockIdx.x, hi = lo + share;
   // ---- the sequence that holds position lo ----
@@ -246,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cur.L = start_len;
     cur.n = n_steps<kStep>(cur.L);
     const long long len1 = length(cur.n);
-    cur.bd = (int)(start_off / len1);
+    cur.bd = (int)div_down(start_off, len1);
     const long long off = start_off - cur.bd * len1;
     cur.left = hi - lo;
     set_part(cur, off);
@@ -509,7 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the shares that hold steps of this bundle
         const long long at = hi - cur.left;                 // the part's line position
         const long long first = at + cur_rest - length(cur.n) + cost;  // of step 0
-        const int c_first = (int)(first / share), c_last = (int)((first + cur.n - 1) / share);
+        const int c_first = (int)div_down(first, share);
+        const int c_last = (int)div_down(first + cur.n - 1, share);
         __threadfence();
         sync();
         if (tg == 0)
@@ -518,43 +532,99 @@ __global__ void __launch_bounds__(kThreads, 1)
         sync();
         if (last_s[gi]) {
           __threadfence();
-          for (int x = tg; x < nh * (D / 4); x += n_tg) {
-            const int h = x / (D / 4), c = x % (D / 4);
-            // 8 parts at a time, all their loads in flight together
-            float M = -INFINITY, L = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int z0 = c_first; z0 <= c_last; z0 += 8) {
-              float2 ml[8];
-              float4 y[8];
+          // only this group's warps are here
+          auto group_sync = [&]() {
+            if (kw == 1)
+              __syncwarp();
+            else
+              named_barrier(1 + gi, n_tg);
+          };
+          // Parts in chunks of D/2.  Their maxima and sums go to shared memory in one
+          // round trip and become weights there; then 16 loads of O in flight a thread.
+          constexpr int kChunk = D / 2, kItems = ROWS * D / 128;
+          float2(*wl)[ROWS] = reinterpret_cast<float2(*)[ROWS]>(join + gi * ROWS * D);
+          static_assert(kChunk * ROWS * sizeof(float2) <= ROWS * D * 4, "a warp's join buffer");
+          auto at_part = [&](int z) {
+            return a.part + (((int64_t)z * 2 + (z == c_first ? 1 : 0)) * kWarps + gi) * Cfg::kPart;
+          };
+          float4 acc[kItems];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int z = z0 + i <= c_last ? z0 + i : c_last;
-                const float* pz =
-                    a.part + (((int64_t)z * 2 + (z == c_first ? 1 : 0)) * kWarps + gi) * Cfg::kPart;
-                ml[i] = __ldcg(reinterpret_cast<const float2*>(pz + ROWS * D + 2 * h));
-                y[i] = __ldcg(reinterpret_cast<const float4*>(pz + h * D + 4 * c));
+          for (int i = 0; i < kItems; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int z0 = c_first; z0 <= c_last; z0 += kChunk) {
+            const int nz = min(kChunk, c_last - z0 + 1);
+            if (z0 > c_first) group_sync();  // the chunk before has been used
+            for (int x = tg; x < nz * ROWS; x += n_tg)
+              if (x % ROWS < nh)
+                wl[x / ROWS][x % ROWS] = __ldcg(reinterpret_cast<const float2*>(
+                    at_part(z0 + x / ROWS) + ROWS * D + 2 * (x % ROWS)));
+            group_sync();
+            if (ki == 0) {
+              // lanes h, h + ROWS, ..: head h
+              const int h = lane % ROWS;
+              const float m0 = z0 > c_first ? jm[gi][h] : -INFINITY;
+              const float l0 = z0 > c_first ? jl[gi][h] : 0.f;
+              float mx = m0;
+              if (h < nh)
+                for (int z = lane / ROWS; z < nz; z += 32 / ROWS) mx = fmaxf(mx, wl[z][h].x);
+#pragma unroll
+              for (int o = ROWS; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              const float mu = mx > -INFINITY ? mx : 0.f;
+              float ls = 0.f;
+              if (h < nh)
+                for (int z = lane / ROWS; z < nz; z += 32 / ROWS) {
+                  const float w = fast_exp2(wl[z][h].x - mu);
+                  ls += w * wl[z][h].y;
+                  wl[z][h].x = w;
+                }
+#pragma unroll
+              for (int o = ROWS; o < 32; o <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+              const float f = fast_exp2(m0 - mu);
+              __syncwarp();
+              if (lane < ROWS) jm[gi][h] = mx, jl[gi][h] = l0 * f + ls, jf[gi][h] = f;
+            }
+            group_sync();
+#pragma unroll
+            for (int i0 = 0; i0 < kItems; i0 += 4) {
+              if (tg + i0 * n_tg >= nh * (D / 4)) break;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float f = jf[gi][min(tg + (i0 + i) * n_tg, nh * (D / 4) - 1) / (D / 4)];
+                acc[i0 + i].x *= f, acc[i0 + i].y *= f, acc[i0 + i].z *= f, acc[i0 + i].w *= f;
               }
-              float mn = M;
+              for (int z = 0; z < nz; z += 4) {
+                float4 y[4][4];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) mn = fmaxf(mn, ml[i].x);
-              const float mu = mn > -INFINITY ? mn : 0.f;
-              const float f0 = fast_exp2(M - mu);
-              L *= f0;
-              acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
+                for (int e = 0; e < 4; ++e) {
+                  const float* pz = at_part(z0 + min(z + e, nz - 1));
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                if (z0 + i <= c_last) {
-                  const float f = fast_exp2(ml[i].x - mu);
-                  L += f * ml[i].y;
-                  acc.x += f * y[i].x, acc.y += f * y[i].y;
-                  acc.z += f * y[i].z, acc.w += f * y[i].w;
+                  for (int i = 0; i < 4; ++i) {
+                    const int x = min(tg + (i0 + i) * n_tg, nh * (D / 4) - 1);
+                    y[e][i] = __ldcg(reinterpret_cast<const float4*>(pz + 4 * x));
+                  }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if (z + e >= nz) continue;
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const int x = min(tg + (i0 + i) * n_tg, nh * (D / 4) - 1);
+                    const float f = wl[z + e][x / (D / 4)].x;
+                    float4& v = acc[i0 + i];
+                    v.x += f * y[e][i].x, v.y += f * y[e][i].y;
+                    v.z += f * y[e][i].z, v.w += f * y[e][i].w;
+                  }
                 }
               }
-              M = mn;
             }
-            const float inv = 1.f / L;
+          }
+#pragma unroll
+          for (int i = 0; i < kItems; ++i) {
+            const int x = tg + i * n_tg;
+            if (x >= nh * (D / 4)) continue;
+            const int h = x / (D / 4), c = x % (D / 4);
+            const float inv = 1.f / jl[gi][h];
             *reinterpret_cast<uint2*>(orow + (int64_t)h * D + 4 * c) = make_uint2(
-                pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
           }
         }
       }
