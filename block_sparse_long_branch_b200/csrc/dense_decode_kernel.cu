@@ -16,8 +16,8 @@
 // registers:
 //   S = Q K^T  mma.m16n8k16: the 16 rows are the group's heads (8 heads: rows 8-15
 //              are zero; 16 heads: all used)
-//   O += P V   P in two bf16 parts, hi = bf16(p) and lo = bf16(p - hi), so the
-//              product sees p to 16 bits: 8 heads put lo into rows 8-15 of the
+//   O += P V   P in two bf16 parts, hi = p cut to 8 bits and lo = bf16(p - hi), so
+//              the product sees p to 2^-16 of itself: 8 heads put lo into rows 8-15 of the
 //              same MMA, 16 heads take a second one.
 // S, the maximum, the sum and O are fp32.
 //
@@ -434,10 +434,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int rr = 0; rr < ROWS / 8; ++rr)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const uint32_t w = pack_bf16x2(p[rr][2 * t], p[rr][2 * t + 1]);
-          hi2[rr][t] = w;
-          lo2[rr][t] = pack_bf16x2(p[rr][2 * t] - __uint_as_float(w << 16),
-                                   p[rr][2 * t + 1] - __uint_as_float(w & 0xFFFF0000u));
+          // hi cut, not rounded, and the last bit of p set: lo > 0 wherever p > 0, so
+          // that an infinity in V stays one (with lo < 0, inf - inf, and with lo = 0,
+          // 0 * inf, are NaN)
+          const uint32_t p0 = __float_as_uint(p[rr][2 * t]) | 1u;
+          const uint32_t p1 = __float_as_uint(p[rr][2 * t + 1]) | 1u;
+          hi2[rr][t] = __byte_perm(p0, p1, 0x7632);
+          lo2[rr][t] = pack_bf16x2(__uint_as_float(p0) - __uint_as_float(p0 & 0xFFFF0000u),
+                                   __uint_as_float(p1) - __uint_as_float(p1 & 0xFFFF0000u));
         }
 #pragma unroll
       for (int kt = 0; kt < NT / 2; ++kt)  // 16 keys

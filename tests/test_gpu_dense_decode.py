@@ -101,6 +101,29 @@ def test_odd_values(msa):
     assert np.isfinite(out[0, :2]).all()
 
 
+@pytest.mark.parametrize("H,G,d", [(4, 2, 64), (8, 1, 128), (32, 2, 128)])
+def test_infinite_values_stay_infinite(msa, H, G, d):
+    """One infinity among the values a row sees makes the output that infinity, not NaN, at
+    whatever key and weight; infinities of both signs make it NaN."""
+    page, lens = 16, [40, 700, 9]
+    k, v, table, tnp = dc.pool(lens, page, G, d, 21)
+    def put(b, s, col, x):
+        v[int(tnp[b, s // page]), s % page, G - 1, col] = x
+    for col in range(8, 40):  # every key of sequence 0 and of sequence 2 in turn
+        put(0, col, col, float("inf"))
+        put(2, col % 9, col, float("-inf"))
+    put(1, 0, 1, float("inf")), put(1, 699, 2, float("-inf")), put(1, 350, 3, float("inf"))
+    put(1, 10, 4, float("inf")), put(1, 690, 4, float("-inf"))
+    q = dc.randn((3, H, d), 5)
+    cfg = msa.config(H, G, d, d)
+    out = msa.msa_dense_decode_paged(cfg, q, msa.paged_kv(k, v, table),
+                                     torch.tensor(lens, dtype=torch.int32).cuda())
+    ref, mag = dense.decode_paged(q, k, v, tnp, lens, cfg.softmax_scale)
+    assert np.isinf(ref).sum() == (2 * 32 + 3) * (H // G) and np.isnan(ref).sum() == H // G
+    dc.check_attention(out, ref, mag, dense.as_f64(q), dense.as_f64(k), cfg.softmax_scale,
+                       max(lens), P_TWO_PARTS)
+
+
 def test_bad_entries_are_recorded(msa):
     H, G, d, page = 4, 2, 64, 16
     lens = [40, 33, 20]
