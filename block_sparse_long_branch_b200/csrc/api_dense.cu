@@ -155,7 +155,8 @@ msa_status_t msa_rope_append_paged(const msa_config_t* cfg, const void* q, int64
   msa_status_t st = check_dense_cfg(cfg);
   if (st != MSA_OK) return st;
   if ((st = check_rows(cfg, T, B)) != MSA_OK) return st;
-  if (!k || !v || (!inv_freq && rot_dim != 0) || !cu_seqlens || !seq_lens || (q == nullptr) != (q_out == nullptr))
+  if (!k || !v || (!inv_freq && rot_dim != 0) || !cu_seqlens || !seq_lens ||
+      (q == nullptr) != (q_out == nullptr))
     return MSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
       (reinterpret_cast<uintptr_t>(inv_freq) & 3) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 7) ||
@@ -166,6 +167,7 @@ msa_status_t msa_rope_append_paged(const msa_config_t* cfg, const void* q, int64
   if ((q && (q_stride < hd || q_stride % 8 != 0)) || k_stride < gd || k_stride % 8 != 0 ||
       v_stride < gd || v_stride % 8 != 0)
     return MSA_ERR_INVALID_ARG;
+  if (q && q == q_out && q_stride != hd && T > 1) return MSA_ERR_INVALID_ARG;
   if (rot_dim < 0 || rot_dim > cfg->head_dim) return MSA_ERR_INVALID_ARG;
   if (rot_dim % 16 != 0) return MSA_ERR_UNSUPPORTED;
   RopeAppendLaunch p{};

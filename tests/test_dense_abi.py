@@ -112,6 +112,13 @@ def test_sizes_and_strides():
     assert append(rot=136) == 1 and append(rot=-16) == 1 and append(rot=24) == 2
 
 
+def test_append_in_place_needs_packed_queries():
+    assert append(qs=1032, q=P, qo=P, n=0) == 1
+    # packed queries, one token, or another output: refused for the workspace only
+    assert append(n=0) == 3 and append(qs=1032, T=1, n=0) == 3
+    assert append(qs=1032, qo=ctypes.c_void_p(1 << 24), n=0) == 3
+
+
 def test_workspaces():
     for call, op, T, B in ((decode, msa.OP_DENSE_DECODE, 2, 2),
                            (paged, msa.OP_DENSE_PREFILL_PAGED, 5, 2),
