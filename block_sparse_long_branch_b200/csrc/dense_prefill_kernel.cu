@@ -19,7 +19,7 @@
 //
 // Precision: S, m, l and O are fp32.  P is rounded to bf16, since V is bf16 in
 // the caller's cache and the two operands of one MMA share a type; each weight is
-// then off by at most 2^-9 of itself, beside the 2^-9 of the bf16 output.
+// then off by at most 2^-8 of itself, beside the 2^-8 of the bf16 output.
 //
 // Rows that a mask hides.  A hidden key has P = 0 exactly, but 0 * NaN = NaN on the
 // tensor cores, so in the tiles that some row of the unit does not see whole
@@ -1028,7 +1028,8 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
   __syncthreads();
   const bool one_wave = (long long)n_units_s * p.G <= p.ctas;
-  const int share = (int)((sum_s * p.G + p.ctas - 1) / p.ctas);
+  // kept far from 2^31, whatever the lengths
+  const int share = (int)min((sum_s * p.G + p.ctas - 1) / p.ctas, 1ull << 29);
   // a unit of one row tile is taken by both softmax warpgroups: half as long
   auto weight = [&](int ntok, int nt) { return ntok <= p.TT ? (nt + 1) / 2 : nt; };
   int part = 1 << 30;  // longest part, by weight
