@@ -59,7 +59,7 @@ constexpr float kGrow = 8.f;  // log2 of the growth of the maximum left unapplie
 constexpr int kFlagSlots = 8;
 constexpr int kTurns = 8;
 constexpr int kUnitTurns = 4;
-constexpr int kDirectUnits = 160;  // as many as CTAs; a multiple of 32
+constexpr int kDirectUnits = 160;  // as many as CTAs
 constexpr int kBoxRows = 128;  // of a TMA copy, at most (smaller boxes gained nothing)
 
 template <int D>
@@ -107,13 +107,13 @@ struct HostSplits {
   DenseSplit s[kHostUnits / 2];
 };
 struct NoUnits {};
-// Paged batches of so few units that they fit the GPU at once: every CTA works out
-// its own from the lengths on the device (direct_plan), with no planning kernel
-// in front.
+// Paged batches of few units: every CTA works out its own from the lengths on the
+// device (direct_plan), with no planning kernel in front.
 struct DirectArgs {
   const int64_t* cu;
   const int32_t* seq_lens;
   int32_t B, T, table_rows, can_split;
+  int32_t max_units;  // as many as T tokens of B sequences make
 };
 template <int MODE>
 using ModeArgs = std::conditional_t<MODE == kHost, HostUnits,
@@ -130,8 +130,15 @@ struct Unit {
 };
 
 struct DirectUnit {
-  DenseUnit d;
-  int g;  // -1: none
+  DenseUnit d;  // slot: of this group
+  int g;        // -1: none
+};
+// Where a CTA is in the line of all units (see direct_plan): unit `off` of sequence
+// `seq` and group `g`, which begins at `start`.
+struct LineState {
+  long long start;
+  int share;  // 0: no line
+  int seq, off, g;
 };
 
 // Unit x of the line of all units (groups innermost, longest first).
@@ -139,8 +146,10 @@ template <int MODE>
 __device__ __forceinline__ void read_unit(const PrefillArgs& a, const ModeArgs<MODE>& hu,
                                           const DirectUnit* own, unsigned x, Unit& u) {
   if constexpr (MODE == kDirect) {
-    u.d = own->d;
-    u.g = own->g;
+    const volatile int* p = reinterpret_cast<const volatile int*>(own);
+    u.d.tok0 = p[0], u.d.ntok = p[1], u.d.pos0 = p[2], u.d.seq = p[3];
+    u.d.kv0 = p[4], u.d.kv1 = p[5], u.d.slot = p[6], u.d.row0 = p[7];
+    u.g = p[8];
   } else {
     const unsigned i = x / (unsigned)a.G;
     u.g = (int)(x - i * (unsigned)a.G);
@@ -152,6 +161,7 @@ __device__ __forceinline__ void read_unit(const PrefillArgs& a, const ModeArgs<M
       u.d.tok0 = x0.x, u.d.ntok = x0.y, u.d.pos0 = x0.z, u.d.seq = x0.w;
       u.d.kv0 = x1.x, u.d.kv1 = x1.y, u.d.slot = x1.z, u.d.row0 = x1.w;
     }
+    if (u.d.slot >= 0) u.d.slot += u.g;
   }
   u.nt = u.d.kv1 - u.d.kv0;
   u.dual = u.d.ntok <= a.TT;
@@ -188,27 +198,59 @@ __host__ __device__ __forceinline__ int part_begin(int k, int parts, int len, in
   return k > 0 && k * len > nt - 2 ? nt - 2 : k * len;
 }
 
-// The plan of few units by one warp, up to 32 sequences: `f` is called by one lane
-// for each unit with its first packed row, tokens, first position, sequence, key
-// tiles, key tiles per part, parts, and the parts of the units before it.  The
-// rules are dense_plan_kernel's for units that fit `ctas` CTAs at once.
-template <typename F>
-__device__ __forceinline__ void direct_plan(const DirectArgs& p, int G, int TT, int ctas,
-                                            uint32_t* err, F&& f) {
-  const int lane = lane_id(), U = 2 * TT;
-  int64_t lo = 0, hi = 0;
-  int L = 0;
-  if (lane < p.B) {
-    lo = __ldg(p.cu + lane);
-    hi = __ldg(p.cu + lane + 1);
-    L = __ldg(p.seq_lens + lane);
-  }
-  int n = (int)(hi - lo), pos = L - n;
-  if (lane < p.B && (lo < 0 || hi < lo || hi > p.T || (n > 0 && (pos < 0 || L > p.table_rows)))) {
+constexpr int kPartCost = 3;  // a unit's or a part's cost beside its key tiles, in key tiles
+constexpr int kJoinCost = 7;  // partial results stored, read and joined, likewise: units of 27
+                              // key tiles split to take 26 lost 8 of 78 us
+
+// new tokens [lo, lo+n) of sequence b, the first at position pos; n = 0: none, or invalid
+__device__ __forceinline__ void direct_seq(const DirectArgs& p, int b, uint32_t* err, int64_t& lo,
+                                           int& n, int& pos) {
+  lo = __ldg(p.cu + b);
+  const int64_t hi = __ldg(p.cu + b + 1);
+  const int L = __ldg(p.seq_lens + b);
+  n = (int)(hi - lo);
+  pos = L - n;
+  if (lo < 0 || hi < lo || hi > p.T || (n > 0 && (pos < 0 || L > p.table_rows))) {
     record_error(err, kDevBadIndex);
     n = 0;
   }
-  const int units = (n + U - 1) / U;
+}
+// key tiles of the unit `off` of a sequence, and its weight: a unit of one row tile
+// is taken by both softmax warpgroups, half as long
+__device__ __forceinline__ int direct_tiles(int n, int pos, int off, int TT, int& w) {
+  const int nt = (pos + min(n, off + 2 * TT) - 1) / kKeys + 1;
+  w = n - off <= TT ? (nt + 1) / 2 : nt;
+  return nt;
+}
+
+// The plan of units that fit the GPU at once, by one warp, up to 32 sequences: either
+//  * as dense_plan_kernel does, all in parts of at most `part`, by weight, one a CTA; or
+//  * the units of all groups as one line, cut into equal shares, one a CTA, which
+//    leaves no CTA idle (100 units of one length do not make 148 parts): where that
+//    shortens the longest CTA's work by an eighth.  It costs the units of a group
+//    their common pace through the keys, which then come from memory several times:
+//    52 units over 30K keys (32 heads in 4 groups) 248 -> 220 us, 109 over 0.1K to
+//    50K (16 heads in one) 201 -> 131, but 512 units over 1K to 30K 735 -> 956.
+struct PlanUnit {
+  int seq, off;  // sequence, first of its new tokens
+  int nt, w;     // key tiles, weight
+  int pre;       // the weights, each with kPartCost, of the units before
+};
+struct DirectPlan {
+  int64_t lo;  // lane b: sequence b
+  int n, pos;
+  int total;   // units, in `u`
+  int part;
+  int share;   // of the line; 0: parts
+  PlanUnit* u;
+};
+__device__ __forceinline__ void direct_plan(const DirectArgs& p, int G, int TT, int ctas,
+                                            uint32_t* err, PlanUnit* tab, DirectPlan& d) {
+  const int lane = lane_id(), U = 2 * TT;
+  d.u = tab;
+  d.lo = 0, d.n = 0, d.pos = 0;
+  if (lane < p.B) direct_seq(p, lane, err, d.lo, d.n, d.pos);
+  const int units = (d.n + U - 1) / U;
   int incl = units;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -216,55 +258,77 @@ __device__ __forceinline__ void direct_plan(const DirectArgs& p, int G, int TT, 
     if (lane >= o) incl += y;
   }
   // offsets that overlap could make more units than the host counted
-  const int total = min(__shfl_sync(0xffffffffu, incl, 31), kDirectUnits);
-  // unit 32 k + lane: its sequence and offset, and its weight (see weight below)
-  struct Own {
-    int seq, off, nt, w;
-  } own[kDirectUnits / 32];
-  int sum = 0, longest = 0;
-#pragma unroll
-  for (int k = 0; k < kDirectUnits / 32; ++k) {
-    own[k].w = 0;
-    if (32 * k >= total) continue;
-    const int x = 32 * k + lane;
+  d.total = min(__shfl_sync(0xffffffffu, incl, 31), p.max_units);
+  int longest = 0, line = 0;
+#pragma unroll 1  // code that runs once: its size is its time
+  for (int k = 0; k < d.total; k += 32) {
+    const int x = k + lane;
     int s = 0;
+#pragma unroll 1
     for (int b = 0; b < p.B; ++b) s += __shfl_sync(0xffffffffu, incl, b) <= x;
     s = min(s, 31);
-    const int off = (x - (__shfl_sync(0xffffffffu, incl, s) - __shfl_sync(0xffffffffu, units, s))) * U;
-    const int len = __shfl_sync(0xffffffffu, n, s), p0 = __shfl_sync(0xffffffffu, pos, s);
-    if (x < total) {
-      own[k].seq = s;
-      own[k].off = off;
-      own[k].nt = (p0 + min(len, off + U) - 1) / kKeys + 1;
-      own[k].w = len - off <= TT ? (own[k].nt + 1) / 2 : own[k].nt;
-      sum += own[k].w;
-      longest = max(longest, own[k].w);
+    PlanUnit u;
+    u.seq = s;
+    u.off = (x - (__shfl_sync(0xffffffffu, incl, s) - __shfl_sync(0xffffffffu, units, s))) * U;
+    const int len = __shfl_sync(0xffffffffu, d.n, s), p0 = __shfl_sync(0xffffffffu, d.pos, s);
+    int c = 0;
+    if (x < d.total) {
+      u.nt = direct_tiles(len, p0, u.off, TT, u.w);
+      longest = max(longest, u.w);
+      c = u.w + kPartCost;
     }
+    int y = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    u.pre = line + y - c;
+    line += __shfl_sync(0xffffffffu, y, 31);
+    if (x < d.total) tab[x] = u;
   }
-  sum = __reduce_add_sync(0xffffffffu, sum);
+  __syncwarp();
   longest = __reduce_max_sync(0xffffffffu, longest);
-  int part = 1 << 30;
-  if (p.can_split) {
-    for (int c = max(kMinPart, (sum * G + ctas - 1) / ctas); c < longest; ++c) {
-      int m = 0;
-#pragma unroll
-      for (int k = 0; k < kDirectUnits / 32; ++k) m += (own[k].w + c - 1) / c;
-      if (__reduce_add_sync(0xffffffffu, m) * G <= ctas) {
-        part = c;
-        break;
-      }
-    }
+  d.part = 1 << 30;
+  d.share = 0;
+  if (!p.can_split) return;
+  const int sum = line - kPartCost * d.total;
+  // the least that makes no more parts than CTAs (their number falls with it): mostly
+  // near the even share, so in growing steps from there, then by halves
+  int c0 = max(kMinPart, (sum * G + ctas - 1) / ctas), c1 = longest, step = 1;
+#pragma unroll 1
+  while (c0 < c1) {
+    const int c = step > 0 && step < c1 - c0 ? c0 + step - 1 : (c0 + c1) / 2;
+    int m = 0;
+#pragma unroll 1
+    for (int x = lane; x < d.total; x += 32) m += ((unsigned)tab[x].w + c - 1) / (unsigned)c;
+    if (__reduce_add_sync(0xffffffffu, m) * G <= ctas)
+      c1 = c, step = 0;
+    else
+      c0 = c + 1, step *= 2;
   }
+  if (c1 + kJoinCost < longest) d.part = c1;
+  const int share = max((line * G + ctas - 1) / ctas, kMinPart + kPartCost);
+  const int parted = d.part < longest ? d.part + kJoinCost : longest;
+  if ((share + kJoinCost) * 8ll < parted * 7ll) d.share = share;
+}
+// The units of the plan in parts: `f` is called by one lane for each with its first
+// packed row, tokens, first position, sequence, key tiles, key tiles per part, parts,
+// and the parts of the units before it.
+template <typename F>
+__device__ __forceinline__ void direct_parts(const DirectPlan& d, int TT, F&& f) {
+  const int lane = lane_id(), U = 2 * TT;
   int pre = 0;
-#pragma unroll
-  for (int k = 0; k < kDirectUnits / 32; ++k) {
-    if (32 * k >= total) continue;
-    const bool mine = 32 * k + lane < total;
+#pragma unroll 1
+  for (int k = 0; k < d.total; k += 32) {
+    const bool mine = k + lane < d.total;
+    PlanUnit u = {};
     int parts = 0, len = 1;
     if (mine) {
-      const int q = own[k].w > part ? (own[k].w + part - 1) / part : 1;
-      len = (own[k].nt + q - 1) / q;
-      parts = (own[k].nt + len - 1) / len;
+      u = d.u[k + lane];
+      const int q = u.w > d.part ? (u.w + d.part - 1) / d.part : 1;
+      len = (u.nt + q - 1) / q;
+      parts = (u.nt + len - 1) / len;
     }
     int x = parts;
 #pragma unroll
@@ -272,14 +336,61 @@ __device__ __forceinline__ void direct_plan(const DirectArgs& p, int G, int TT, 
       const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    const int s = mine ? own[k].seq : 0;
-    const int64_t a = __shfl_sync(0xffffffffu, (long long)lo, s);
-    const int p0 = __shfl_sync(0xffffffffu, pos, s), ln = __shfl_sync(0xffffffffu, n, s);
-    if (mine)
-      f(a + own[k].off, min(U, ln - own[k].off), p0 + own[k].off, s, own[k].nt, len, parts,
-        pre + x - parts);
+    const int64_t a = __shfl_sync(0xffffffffu, (long long)d.lo, u.seq);
+    const int p0 = __shfl_sync(0xffffffffu, d.pos, u.seq), ln = __shfl_sync(0xffffffffu, d.n, u.seq);
+    if (mine) f(a + u.off, min(U, ln - u.off), p0 + u.off, u.seq, u.nt, len, parts, pre + x - parts);
     pre += __shfl_sync(0xffffffffu, x, 31);
   }
+}
+// First key tile behind line offset x of a unit that takes `len` of the line: what
+// would be a crumb of less than three tiles goes with the rest (the last part has
+// two tiles at least: see part_begin).
+__device__ __forceinline__ int line_cut(long long x, int len, int nt) {
+  if (x <= 0) return 0;
+  if (x >= len) return nt;
+  const long long y = x * nt;
+  const int t = (int)((y >> 32) == 0 ? (unsigned)y / (unsigned)len : y / len);
+  return t < 3 ? 0 : t > nt - 3 ? nt : t;
+}
+// The next part of this CTA's share of the line; g = -1: none.  A whole warp.  Partial
+// results: slot 2c of CTA c holds the unit that began in an earlier share, 2c + 1 the
+// one that goes on in a later.
+__device__ __forceinline__ void line_next(const DirectArgs& p, int G, int TT,
+                                          volatile LineState& st, DirectUnit& out) {
+  const int share = st.share;
+  const long long lo = (long long)blockIdx.x * share, hi = lo + share;
+  int s = st.seq, off = st.off, g = st.g;
+  long long start = st.start;
+  int64_t a = 0;
+  int n = 0, pos = 0;
+  out.g = -1;
+  if (s < p.B) direct_seq(p, s, nullptr, a, n, pos);
+  while (s < p.B && start < hi && out.g < 0) {
+    if (off >= n) {
+      off = 0;
+      if (++s < p.B) direct_seq(p, s, nullptr, a, n, pos);
+      continue;
+    }
+    int w;
+    const int nt = direct_tiles(n, pos, off, TT, w), len = w + kPartCost;
+    const int kv0 = line_cut(lo - start, len, nt), kv1 = line_cut(hi - start, len, nt);
+    if (kv0 < kv1) {
+      out.d = DenseUnit{(int)a + off, min(2 * TT, n - off), pos + off, s, kv0, kv1, -1, 0};
+      if (kv0 > 0)
+        out.d.slot = 2 * blockIdx.x;
+      else if (kv1 < nt)
+        out.d.slot = 2 * blockIdx.x + 1;
+      out.g = g;
+    }
+    start += len;
+    if (++g == G) g = 0, off += 2 * TT;
+  }
+  __syncwarp();
+  if (lane_id() == 0) {
+    st.start = start;
+    st.seq = s, st.off = off, st.g = g;
+  }
+  __syncwarp();
 }
 
 template <int D, int MODE>
@@ -308,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t bar_drain[2];
   __shared__ uint64_t bar_half_done, bar_half_read;  // dual units: tile 1's result, and its reading
   __shared__ float half_m[kRows], half_l[kRows];
-  __shared__ DirectUnit own_s;
+  __shared__ DirectUnit own_s[MODE == kDirect ? kUnitTurns : 1];
+  __shared__ LineState line_s;
   // the CTA's units after its first: handed out by warp 8
   __shared__ uint64_t bar_u_full[kUnitTurns], bar_u_empty[kUnitTurns];
   __shared__ unsigned unit_s[kUnitTurns];
@@ -354,21 +466,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&map_q);
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
-    own_s.g = -1;
+    own_s[0].g = -1;
+    line_s.share = 0;
+    line_s.seq = 1 << 30;  // of a share behind the line's end
+    line_s.off = line_s.g = 0;
+    line_s.start = 0;
   }
   if constexpr (MODE == kDirect) {
     if (warp == 1) {
       __syncwarp();
-      const int i = blockIdx.x / a.G;
-      direct_plan(hu, a.G, a.TT, gridDim.x, a.err,
-                  [&](int64_t tok0, int ntok, int pos0, int seq, int nt, int len, int parts, int pre) {
-                    if (i < pre || i >= pre + parts) return;
-                    const int k = i - pre;
-                    own_s.d = DenseUnit{(int)tok0, ntok, pos0, seq, part_begin(k, parts, len, nt),
-                                        part_begin(k + 1, parts, len, nt),
-                                        parts > 1 ? i * a.G : -1, 0};
-                    own_s.g = blockIdx.x - i * a.G;
-                  });
+      // the units in what will be a Q tile
+      PlanUnit* tab = reinterpret_cast<PlanUnit*>(sQ);
+      static_assert(kDirectUnits * sizeof(PlanUnit) <= Cfg::kTileBytes, "the plan's units");
+      DirectPlan d;
+      direct_plan(hu, a.G, a.TT, gridDim.x, a.err, tab, d);
+      if (d.share == 0) {
+        const int i = blockIdx.x / a.G;
+        direct_parts(d, a.TT, [&](int64_t tok0, int ntok, int pos0, int seq, int nt, int len,
+                                  int parts, int pre) {
+          if (i < pre || i >= pre + parts) return;
+          const int k = i - pre, g = blockIdx.x - i * a.G;
+          own_s[0].d = DenseUnit{(int)tok0, ntok, pos0, seq, part_begin(k, parts, len, nt),
+                                 part_begin(k + 1, parts, len, nt), parts > 1 ? i * a.G + g : -1, 0};
+          own_s[0].g = g;
+        });
+      } else {
+        // the unit that holds this share's first position
+        const long long lo = (long long)blockIdx.x * d.share;
+#pragma unroll 1
+        for (int x = lane; x < d.total; x += 32) {
+          const int len = tab[x].w + kPartCost;
+          const long long from = (long long)tab[x].pre * a.G;
+          if (lo < from || lo >= from + (long long)len * a.G) continue;
+          line_s.seq = tab[x].seq;
+          line_s.off = tab[x].off;
+          line_s.g = (int)((unsigned)(lo - from) / (unsigned)len);
+          line_s.start = from + (long long)line_s.g * len;
+        }
+        if (lane == 0) line_s.share = d.share;
+      }
+      fence_async_smem();  // the Q tile's memory goes to TMA
     }
   }
   if (warp == 0) {
@@ -385,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (MODE == kHost) {
     total = hu.n * a.G;
   } else if constexpr (MODE == kDirect) {
-    total = own_s.g >= 0 ? 1 : 0;
+    total = 0;  // see next_unit
   } else {
     pdl_wait();  // for the units
     total = __ldcg(a.n_units) * a.G;
@@ -395,34 +532,53 @@ __global__ void __launch_bounds__(kThreads, 1)
   // and takes the next one of the line whenever it has loaded a unit: longest
   // first, so the CTAs end nearly together whatever the lengths (chunks of four
   // caches of 1K to 30K: 917 -> 830 us against a fixed order).
+  // With kDirect warp 8 hands out the CTA's own unit, or the parts of its share.
   auto next_unit = [&](int r, Unit& u) {
-    unsigned x = MODE == kDirect ? 0 : blockIdx.x;  // kDirect: total is 1 or 0
-    if (r > 0) {
-      if (MODE == kDirect || total <= (int)gridDim.x) return false;
-      const int turn = (r - 1) % kUnitTurns;
-      const uint32_t phase = ((r - 1) / kUnitTurns) & 1;
+    constexpr bool kOwn = MODE == kDirect;
+    unsigned x = blockIdx.x;
+    const DirectUnit* own = own_s;
+    const int q = kOwn ? r : r - 1;
+    const int turn = q % kUnitTurns;
+    if (kOwn || r > 0) {
+      if (!kOwn && total <= (int)gridDim.x) return false;
+      const uint32_t phase = (q / kUnitTurns) & 1;
       if (warp == kLoadWarp) {
         if (!__all_sync(0xffffffffu, mbar_wait(&bar_u_empty[turn], phase ^ 1, abort_flag, a.err,
                                                kDevTimeoutConsumer)))
           return false;
-        if (lane == 0) {
-          x = atomicAdd(a.next_unit, 1) + gridDim.x;
-          unit_s[turn] = x;
-          mbar_arrive(&bar_u_full[turn]);
+        if constexpr (kOwn) {
+          if (line_s.share > 0) {
+            DirectUnit next;
+            line_next(hu, a.G, a.TT, line_s, next);
+            if (lane == 0) own_s[turn] = next;
+          } else if (r > 0 && lane == 0) {
+            own_s[turn].g = -1;
+          }
+          if (lane == 0) mbar_arrive(&bar_u_full[turn]);
+          __syncwarp();
+        } else {
+          if (lane == 0) {
+            x = atomicAdd(a.next_unit, 1) + gridDim.x;
+            unit_s[turn] = x;
+            mbar_arrive(&bar_u_full[turn]);
+          }
+          x = __shfl_sync(0xffffffffu, x, 0);
         }
-        x = __shfl_sync(0xffffffffu, x, 0);
       } else {
         if (!__all_sync(0xffffffffu, mbar_wait(&bar_u_full[turn], phase, abort_flag, a.err,
                                                kDevTimeoutLoad)))
           return false;
-        x = *reinterpret_cast<volatile unsigned*>(&unit_s[turn]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_u_empty[turn]);
+        if constexpr (!kOwn) x = *reinterpret_cast<volatile unsigned*>(&unit_s[turn]);
       }
+      if constexpr (kOwn) own = own_s + turn;
     }
-    if (x >= (unsigned)total) return false;
-    read_unit<MODE>(a, hu, &own_s, x, u);
-    return true;
+    const bool any = kOwn || x < (unsigned)total;
+    if (any) read_unit<MODE>(a, hu, own, x, u);
+    if (kOwn || r > 0) {  // read: the turn is free again
+      __syncwarp();
+      if (warp != kLoadWarp && lane == 0) mbar_arrive(&bar_u_empty[turn]);
+    }
+    return any && (!kOwn || u.g >= 0);
   };
 
   if (warp >= 8) {
@@ -888,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (u.d.slot >= 0) {
         // one part of a split unit: O unnormalised, with its maximum (log2 domain) and sum
-        const int64_t prow = ((int64_t)u.d.slot + u.g) * 2 * kRows + i * kRows + row;
+        const int64_t prow = (int64_t)u.d.slot * 2 * kRows + i * kRows + row;
         float* dst = a.part_o + prow * D;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -1056,7 +1212,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       __syncthreads();
       if (found < 1 << 30) break;
     }
-    part = part_s;
+    if (part_s + kJoinCost < longest_s) part = part_s;
   } else if (longest_s > share + share / 4) {
     part = max(share, kMinPart);
   }
@@ -1122,6 +1278,12 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // out = sum_z 2^(m_z - M) O_z / sum_z 2^(m_z - M) l_z over the partials z of every
 // split unit; a warp per row, D/32 columns a lane.
+struct Join {
+  int tok0, ntok, g, parts;
+  int slot0, slot1, step;  // slots of parts 0, 1, 1 + step, ..
+};
+constexpr int kJoins = 160;  // one per CTA at most: each begins in one of its own; a multiple of 32
+
 template <int D, int MODE>
 __global__ void __launch_bounds__(256)
     dense_combine_kernel(const __grid_constant__ std::conditional_t<
@@ -1132,18 +1294,59 @@ __global__ void __launch_bounds__(256)
                          __nv_bfloat16* out) {
   const int HG = H / G;
   int n;
+  // kDirect: by the CTA whose part is the first, and these CTAs in order (every block
+  // makes the table for itself, so its order must not depend on timing)
+  __shared__ Join table[MODE == kDirect ? kJoins : 1];
+  __shared__ int list[MODE == kDirect ? kJoins : 1];
   if constexpr (MODE == kDirect) {
-    __shared__ DenseSplit table[kDirectUnits];
-    __shared__ int n_s;
-    splits = table;
-    if (threadIdx.x == 0) n_s = 0;
+    __shared__ PlanUnit unit_s[kDirectUnits];
+    __shared__ int2 seq_s[32];  // first packed row, tokens
+    __shared__ int n_s, share_s, total_s;
+    for (int i = threadIdx.x; i < kJoins; i += blockDim.x) table[i].parts = 0;
     __syncthreads();
-    if (warp_id() == 0)
-      direct_plan(hs, G, TT, ctas, nullptr,
-                  [&](int64_t tok0, int ntok, int, int, int, int, int parts, int pre) {
-                    if (parts > 1)
-                      table[atomicAdd(&n_s, 1)] = DenseSplit{(int)tok0, ntok, pre * G, parts};
-                  });
+    if (warp_id() == 0) {
+      DirectPlan d;
+      direct_plan(hs, G, TT, ctas, nullptr, unit_s, d);
+      seq_s[lane_id()] = make_int2((int)d.lo, d.n);
+      if (lane_id() == 0) share_s = d.share, total_s = d.total;
+      if (d.share == 0) {
+        direct_parts(d, TT, [&](int64_t tok0, int ntok, int, int, int, int, int parts, int pre) {
+          if (parts <= 1) return;
+          for (int g = 0, c = pre * G; g < G && c < kJoins; ++g, ++c)
+            table[c] = Join{(int)tok0, ntok, g, parts, c, c + G, G};
+        });
+      }
+    }
+    __syncthreads();
+    if (share_s > 0) {  // which units the shares' ends cut
+      for (int x = threadIdx.x; x < total_s * G; x += blockDim.x) {
+        const PlanUnit u = unit_s[x / G];
+        const int g = x % G, len = u.w + kPartCost;
+        const long long start = (long long)u.pre * G + (long long)g * len;
+        int z = (int)(start / share_s);
+        int first = -1, cuts = 0;
+        for (;; ++z) {
+          const int t = line_cut((long long)(z + 1) * share_s - start, len, u.nt);
+          if (t >= u.nt) break;
+          if (t == 0) continue;
+          if (cuts == 0) first = z;
+          ++cuts;
+        }
+        if (cuts > 0 && first < kJoins)
+          table[first] = Join{seq_s[u.seq].x + u.off, min(2 * TT, seq_s[u.seq].y - u.off), g,
+                              cuts + 1, 2 * first + 1, 2 * (first + 1), 2};
+      }
+      __syncthreads();
+    }
+    if (warp_id() == 0) {
+      int k = 0;
+      for (int c = lane_id(); c < kJoins; c += 32) {
+        const unsigned m = __ballot_sync(0xffffffffu, table[c].parts > 0);
+        if (table[c].parts > 0) list[k + __popc(m & ((1u << lane_id()) - 1))] = c;
+        k += __popc(m);
+      }
+      if (lane_id() == 0) n_s = k;
+    }
     __syncthreads();
     n = n_s;
     pdl_wait();
@@ -1155,30 +1358,33 @@ __global__ void __launch_bounds__(256)
     n = __ldcg(counts + 1);
   }
   const int per_tile = TT * HG, per_unit = 2 * per_tile;  // rows
-  const unsigned rows = (unsigned)n * G * per_unit;       // at most (CTAs / 2) * 256
+  const int joins = MODE == kDirect ? n : n * G;
+  const unsigned rows = (unsigned)joins * per_unit;  // at most CTAs * 256
   const int lane = lane_id();
   constexpr int C = D / 32;
   for (unsigned x = blockIdx.x * 8 + warp_id(); x < rows; x += gridDim.x * 8) {
     const unsigned y = x / per_unit;
     const int urow = (int)(x - y * per_unit);
-    const int g = (int)(y % G);
-    int4 sp;
-    if constexpr (MODE != kPlanned) {
-      const DenseSplit* d;
-      if constexpr (MODE == kHost)
-        d = hs.s + y / G;
-      else
-        d = splits + y / G;
-      sp = make_int4(d->tok0, d->ntok, d->slot, d->parts);
+    Join jn;
+    if constexpr (MODE == kDirect) {
+      jn = table[list[y]];
     } else {
-      sp = __ldcg(reinterpret_cast<const int4*>(splits + y / G));
+      const int g = (int)(y % G);
+      int4 sp;
+      if constexpr (MODE == kHost) {
+        const DenseSplit* d = hs.s + y / G;
+        sp = make_int4(d->tok0, d->ntok, d->slot, d->parts);
+      } else {
+        sp = __ldcg(reinterpret_cast<const int4*>(splits + y / G));
+      }
+      jn = Join{sp.x, sp.y, g, sp.w, sp.z + g, sp.z + G + g, G};
     }
     const int tok = urow / HG, hh = urow - tok * HG;
-    if (tok >= sp.y) continue;
+    if (tok >= jn.ntok) continue;
     const int prow = tok >= TT ? kRows + urow - per_tile : urow;  // row of the partial
-    const int np = sp.w;
+    const int np = jn.parts;
     auto at = [&](int z) {  // row of partial z
-      return ((int64_t)sp.z + (int64_t)z * G + g) * 2 * kRows + prow;
+      return (int64_t)(z == 0 ? jn.slot0 : jn.slot1 + (z - 1) * jn.step) * 2 * kRows + prow;
     };
     float M = -INFINITY, L = 0.f, acc[C];
 #pragma unroll
@@ -1226,7 +1432,7 @@ __global__ void __launch_bounds__(256)
       }
     }
     const float inv = 1.f / L;
-    __nv_bfloat16* o = out + (((int64_t)sp.x + tok) * H + g * HG + hh) * D + lane * C;
+    __nv_bfloat16* o = out + (((int64_t)jn.tok0 + tok) * H + jn.g * HG + hh) * D + lane * C;
     if constexpr (C == 4) {
       *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
                                                 pack_bf16x2(acc[2] * inv, acc[3] * inv));
@@ -1287,7 +1493,7 @@ bool host_plan(const DensePrefillLaunch& p, int TT, HostUnits& hu, HostSplits& h
         int64_t m = 0;
         for (int i = 0; i < n; ++i) m += (w[i] + c - 1) / c;
         if (m * p.G <= ctas) {
-          part = c;
+          if (c + kJoinCost < longest) part = c;
           break;
         }
       }
@@ -1382,8 +1588,10 @@ cudaError_t launch_impl(const DensePrefillLaunch& p, cudaStream_t s, int* launch
   a.err = p.err;
   // a warp per row of the split units, as far as there can be rows (those of
   // tokens that a unit lacks included)
-  const int64_t rows = min64(p.T * p.H + (int64_t)p.B * p.G * 2 * kRows, (int64_t)p.grid * kRows);
+  const int64_t rows = min64(p.T * p.H + (int64_t)p.B * p.G * 2 * kRows, (int64_t)p.grid * 2 * kRows);
   const int combine_grid = (int)min64((rows + 7) / 8, (int64_t)p.grid * 16);
+  // every block plans for itself: no more than are resident
+  const int direct_grid = (int)min64(combine_grid, (int64_t)p.grid * 3);
 
   HostUnits hu;
   HostSplits hs;
@@ -1411,7 +1619,8 @@ cudaError_t launch_impl(const DensePrefillLaunch& p, cudaStream_t s, int* launch
   const int table_rows = paged ? (int)min64((int64_t)p.cache.table_stride * p.cache.page_size,
                                             (int64_t)1 << 30)
                                : 0;
-  if (p.cu && p.B <= 32 && (p.T / (2 * TT) + p.B) * p.G <= min64(p.grid, kDirectUnits)) {
+  const int64_t most = p.T / (2 * TT) + p.B;  // units, of one group
+  if (p.cu && p.B <= 32 && most * p.G <= min64(p.grid, kDirectUnits)) {
     if ((e = cudaMemsetAsync(p.err, 0, sizeof(uint32_t), s)) != cudaSuccess) return e;
     DirectArgs da;
     da.cu = p.cu;
@@ -1420,13 +1629,14 @@ cudaError_t launch_impl(const DensePrefillLaunch& p, cudaStream_t s, int* launch
     da.T = (int32_t)p.T;
     da.table_rows = table_rows;
     da.can_split = p.max_slots > 0;
+    da.max_units = (int32_t)most;
     auto kern = dense_prefill_kernel<D, kDirect>;
     if ((e = prepare(kern, Cfg::kSmem)) != cudaSuccess) return e;
     kern<<<p.grid, kThreads, Cfg::kSmem, s>>>(mq, mk, mv, a, da);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ++*launches;
     if (p.max_slots > 0) {
-      e = launch_early(dense_combine_kernel<D, kDirect>, combine_grid, 256, 0, s, da,
+      e = launch_early(dense_combine_kernel<D, kDirect>, direct_grid, 256, 0, s, da,
                        (const DenseSplit*)nullptr, (const int32_t*)nullptr, (const float*)p.part_o,
                        (const float2*)p.part_ml, p.H, p.G, TT, p.grid, a.out);
       if (e != cudaSuccess) return e;

@@ -122,6 +122,18 @@ def test_paged_few_rows_over_long_caches_are_split(msa):
     run_paged(msa, 16, 2, 64, 64, [1], [9001])
 
 
+@pytest.mark.parametrize("H,G,d,page,new,ctx", [
+    (16, 2, 64, 16, [700, 560, 3], [4200, 3600, 9000]),
+    (16, 1, 128, 128, [900, 0, 520], [4100, 30, 4500]),
+    (9, 3, 128, 32, [1300, 1000], [4200, 4600]),
+])
+def test_paged_units_that_do_not_fill_the_gpu_are_cut_into_even_shares(msa, H, G, d, page, new, ctx):
+    """Units of tens of key tiles, too few for a CTA each and too many for two parts each: shares
+    begin and end inside units, and several parts of a unit are joined."""
+    a = run_paged(msa, H, G, d, page, new, ctx, pad=2)
+    assert torch.equal(a, run_paged(msa, H, G, d, page, new, ctx, pad=2))
+
+
 @pytest.mark.parametrize("H,G,d", [(8, 2, 64), (5, 1, 128)])
 def test_paged_many_sequences_are_planned_on_the_device(msa, H, G, d):
     """More than 32 sequences: a planning kernel, units longest first, a long one split."""
