@@ -174,7 +174,8 @@ msa_status_t msa_rope_append_paged(const msa_config_t* cfg, const void* q, int64
   if ((st = check_cache(cfg, cache, &p.cache)) != MSA_OK) return st;
   if (!ws || ws_bytes < kHeader || !aligned16(ws)) return MSA_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), s) != cudaSuccess) return cuda_status(cudaErrorUnknown);
+  if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), s) != cudaSuccess)
+    return cuda_status(cudaErrorUnknown);
   p.q = q;
   p.k = k;
   p.v = v;
@@ -292,8 +293,6 @@ msa_status_t msa_dense_decode_paged(const msa_config_t* cfg, const void* q,
   const DecodeWs w = decode_ws(cfg, B);
   if (!ws || !aligned16(ws) || ws_bytes < w.total) return MSA_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // the error word and the tickets
-  if (cudaMemsetAsync(ws, 0, w.part, s) != cudaSuccess) return cuda_status(cudaErrorUnknown);
   p.q = q;
   p.seq_lens = seq_lens;
   p.B = B;
@@ -305,9 +304,10 @@ msa_status_t msa_dense_decode_paged(const msa_config_t* cfg, const void* q,
   p.tickets = at<int32_t>(ws, w.tickets);
   p.part = at<float>(ws, w.part);
   p.err = at<uint32_t>(ws, 0);
+  p.clear_words = (int32_t)(w.part / 4);
   p.grid = grid_ctas();
   st = cuda_status(launch_dense_decode(p, s));
-  set_launch_count(1);
+  set_launch_count(2);
   return st;
 }
 

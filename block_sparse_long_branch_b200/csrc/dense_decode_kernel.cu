@@ -23,6 +23,7 @@
 //
 // A key past the sequence's end has P = 0, and its V row (memory that may hold
 // anything) is zeroed in shared memory first, since 0 * NaN = NaN.
+#include "early.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
 #include "tmap.h"
@@ -88,7 +89,7 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
 __device__ __forceinline__ int seq_len(const Args& a, int b) {
   const int L = __ldg(a.seq_lens + b);
   if (L < 0 || (int64_t)L > (int64_t)a.table_stride * a.page_size) {
-    record_error(a.err, kDevBadIndex);
+    record_error_early(a.err, kDevBadIndex);
     return 0;
   }
   return L;
@@ -223,7 +224,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (found && tid == me) start_b = b, start_len = len, start_off = lo - before;
       base += sum;
     }
-    if (lo >= base) return;  // the line ends before this share: the same for all threads
+    if (lo >= base) {  // the line ends before this share: the same for all threads
+      pdl_wait();
+      return;
+    }
   }
   __syncthreads();
 
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < n; ++b, dst += box_rows * 128) {
       int pg = __shfl_sync(0xffffffffu, pages, ld_k % ahead * boxes + b);
       if (pg < 0 || pg >= a.num_pages) {
-        record_error(a.err, kDevBadIndex);
+        record_error_early(a.err, kDevBadIndex);
         pg = a.num_pages;  // outside the tensor: reads zeros
       }
       const int row = (key0 + b * box_rows) % a.page_size;
@@ -317,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 #pragma unroll 1
   for (int s = 0; s < Cfg::kStages; ++s) load();
+  pdl_wait();  // for the cleared error word and tickets
 
   constexpr int NT = kStep / 8;
   const int gq = lane >> 2, tq = lane & 3;
@@ -676,10 +681,11 @@ cudaError_t launch_impl(const DenseDecodeLaunch& p, cudaStream_t s) {
   a.part = p.part;
   a.err = p.err;
   auto kern = dense_decode_kernel<D, ROWS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+  cudaError_t e = launch_clear(p.err, p.clear_words, s);
   if (e != cudaSuccess) return e;
-  kern<<<p.grid, kThreads, Cfg::kSmem, s>>>(mk, mv, a);
-  return cudaGetLastError();
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_early(kern, p.grid, kThreads, Cfg::kSmem, s, mk, mv, a);
 }
 
 }  // namespace

@@ -41,6 +41,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "early.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
 #include "tmap.h"
@@ -1440,24 +1441,6 @@ __global__ void __launch_bounds__(256)
       *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
     }
   }
-}
-
-// A launch that may start while the kernel before it in the stream still runs
-// (the kernel calls pdl_wait before it touches what that one writes).
-template <typename... Params, typename... Args>
-cudaError_t launch_early(void (*kern)(Params...), int grid, int threads, int smem, cudaStream_t s,
-                         Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
 // The plan of a batch with host offsets, by the rules of dense_plan_kernel; false

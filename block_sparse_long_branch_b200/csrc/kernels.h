@@ -268,9 +268,10 @@ struct DenseDecodeLaunch {
   int32_t B, H, G, d;
   float scale;
   void* out;         // [B][H][d]
-  int32_t* tickets;  // [B][head chunks], zero at launch
+  int32_t* tickets;  // [B][head chunks]
   float* part;       // [grid][2][kDenseDecodeWarps][dense_decode_partial_floats()]
   uint32_t* err;
+  int32_t clear_words;  // zeroed first: from the error word to the last ticket
   int grid;
 };
 constexpr int kDenseDecodeWarps = 8;

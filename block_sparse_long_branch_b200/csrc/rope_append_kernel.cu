@@ -12,7 +12,7 @@
 // Memory bound: every element is read and written once.  A CTA takes a few tokens:
 // their rows in the cache and their sines and cosines first, then 16 dimensions of
 // a head per thread and turn (two 16-byte pieces that hold 8 whole pairs in either
-// layout).  A 32K prompt of 64 + 2 x 8 heads of 128 moves at 5.8 TB/s.
+// layout).  A 32K prompt of 64 + 2 x 8 heads of 128 moves at 5.8 to 6.2 TB/s.
 #include "kernels.h"
 #include "sm100.cuh"
 
