@@ -304,7 +304,7 @@ msa_status_t msa_dense_decode_paged(const msa_config_t* cfg, const void* q,
   p.tickets = at<int32_t>(ws, w.tickets);
   p.part = at<float>(ws, w.part);
   p.err = at<uint32_t>(ws, 0);
-  p.clear_words = (int32_t)(w.part / 4);
+  p.clear_words = (int64_t)(w.part / 4);
   p.grid = grid_ctas();
   st = cuda_status(launch_dense_decode(p, s));
   set_launch_count(2);

@@ -32,14 +32,14 @@ cudaError_t launch_early(void (*kern)(Params...), int grid, int threads, int sme
 // before it records an error, takes a ticket or ends (decode of one request of 4K:
 // 18.5 -> 16.4 us back to back).  It costs the host 2 us more than a memset does, so
 // calls that the host bounds have one (append of 16 tokens: 13.8 -> 15.8 us).
-static __global__ void __launch_bounds__(256) clear_kernel(uint4* p, int words) {
+static __global__ void __launch_bounds__(256) clear_kernel(uint4* p, int64_t words) {
   pdl_launch_dependents();
-  const int i = blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (4 * i < words) p[i] = make_uint4(0, 0, 0, 0);
 }
 // words: a multiple of 4
-static inline cudaError_t launch_clear(void* p, int words, cudaStream_t s) {
-  clear_kernel<<<(words / 4 + 255) / 256, 256, 0, s>>>(static_cast<uint4*>(p), words);
+static inline cudaError_t launch_clear(void* p, int64_t words, cudaStream_t s) {
+  clear_kernel<<<(unsigned)((words / 4 + 255) / 256), 256, 0, s>>>(static_cast<uint4*>(p), words);
   return cudaGetLastError();
 }
 

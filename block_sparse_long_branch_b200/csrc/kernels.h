@@ -271,7 +271,7 @@ struct DenseDecodeLaunch {
   int32_t* tickets;  // [B][head chunks]
   float* part;       // [grid][2][kDenseDecodeWarps][dense_decode_partial_floats()]
   uint32_t* err;
-  int32_t clear_words;  // zeroed first: from the error word to the last ticket
+  int64_t clear_words;  // zeroed first: from the error word to the last ticket
   int grid;
 };
 constexpr int kDenseDecodeWarps = 8;

@@ -32,10 +32,10 @@
  *    returns MSA_ERR_CUDA.  Kernels never trap: a wait that runs out, a bad
  *    index or an input value out of range is recorded in a device error word
  *    inside the workspace and read back with msa_get_device_error.
- *  - Supported shapes (the full-attention calls state their own): block_size 128; head_dim and index_dim 64 or 128;
+ *  - Supported shapes: block_size 128; head_dim and index_dim 64 or 128;
  *    1 <= top_k <= 32; G divides 128; H/G is a power of two with
  *    (H/G) * head_dim <= 2048; 1 <= N < 2^26.  Others return
- *    MSA_ERR_UNSUPPORTED.
+ *    MSA_ERR_UNSUPPORTED.  The full-attention calls state their own.
  *  - Readings where the pages are silent: the token score is the raw dot
  *    product (no scale); "visible" means key s <= query t; k includes the
  *    local block; equal pooled scores go to the lower block id; ids are
@@ -466,7 +466,8 @@ typedef struct {
  *     multiple of 16, at most d; dimensions from rot_dim on are copied (0: all
  *     of them, and inv_freq may be NULL).
  *   interleaved: 0 pairs dimension j with j + rot_dim/2, otherwise 2j with 2j+1.
- *   q_out [T][H][d] bf16 out; may be q itself when q_stride is H*d.
+ *   q_out [T][H][d] bf16 out; may be q itself when q_stride is H*d (refused
+ *     otherwise).
  *   cache: k (rotated) and v rows are written; nothing else of it is.
  *   ws: at least msa_workspace_size(cfg, MSA_OP_ROPE_APPEND, T, B).
  */
