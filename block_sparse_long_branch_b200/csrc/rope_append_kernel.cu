@@ -101,7 +101,7 @@ constexpr int kMaxTok = 16;
 template <int D, bool IL>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const Args a, const int tok) {
   constexpr int kItems = D / 16;     // 16-dimension items of a head
-  __shared__ float2 cs[kMaxTok][D / 2];  // (cos, sin)
+  __shared__ alignas(16) float2 cs[kMaxTok][D / 2];  // (cos, sin), read two at a time
   __shared__ int64_t off_s[kMaxTok], pos_s[kMaxTok];
   const int tid = threadIdx.x;
   const int64_t t0 = (int64_t)blockIdx.x * tok;
