@@ -174,8 +174,6 @@ msa_status_t msa_rope_append_paged(const msa_config_t* cfg, const void* q, int64
   if ((st = check_cache(cfg, cache, &p.cache)) != MSA_OK) return st;
   if (!ws || ws_bytes < kHeader || !aligned16(ws)) return MSA_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), s) != cudaSuccess)
-    return cuda_status(cudaErrorUnknown);
   p.q = q;
   p.k = k;
   p.v = v;

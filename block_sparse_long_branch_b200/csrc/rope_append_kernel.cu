@@ -49,6 +49,7 @@ struct Args {
   int64_t T;
   uint8_t* q_out;
   uint32_t* err;
+  bool checked;  // the last CTA checks the batch (check_batch)
 };
 
 // Where token t's row is: its position (-1: of no sequence, or of an invalid one)
@@ -83,16 +84,52 @@ __device__ __forceinline__ void locate(const Args& a, int64_t t, int row_elems, 
   // or a row past the block table
   if (t < begin || t >= end || p < t - begin ||
       p >= (int64_t)a.cache.table_stride * a.cache.page_size) {
-    if (lane == 0) record_error(a.err, kDevBadIndex);
+    if (lane == 0 && !a.checked) record_error(a.err, kDevBadIndex);
     return;
   }
   pos = p;
   const int pg = __ldg(a.cache.block_table + (int64_t)b * a.cache.table_stride + p / a.cache.page_size);
   if (pg < 0 || pg >= a.cache.num_pages) {
-    if (lane == 0) record_error(a.err, kDevBadIndex);
+    if (lane == 0 && !a.checked) record_error(a.err, kDevBadIndex);
     return;
   }
   off = (int64_t)pg * a.cache.page_stride + (p % a.cache.page_size) * (int64_t)row_elems;
+}
+
+// The error word of a batch of up to kThreads sequences, written whole by one CTA that
+// looks at every length and page id while the others work: no memset in front of the
+// kernel (16 tokens: 13.6 -> 12.7 us, the rest of it the host's).  A thread per sequence; pages beyond a sequence's
+// second by the warps.
+__device__ __forceinline__ void check_batch(const Args& a) {
+  __shared__ int long_s[kThreads], n_long;
+  const int b = threadIdx.x, ps = a.cache.page_size;
+  if (b == 0) n_long = 0;
+  __syncthreads();
+  auto bad_page = [&](int seq, int64_t p) {
+    const int pg = __ldg(a.cache.block_table + (int64_t)seq * a.cache.table_stride + p);
+    return pg < 0 || pg >= a.cache.num_pages;
+  };
+  bool bad = false;
+  if (b < a.B) {
+    const int64_t lo = __ldg(a.cu + b), hi = __ldg(a.cu + b + 1);
+    const int64_t L = __ldg(a.seq_lens + b), first = L - (hi - lo);
+    if (lo < 0 || hi < lo || hi > a.T ||
+        (hi > lo && (first < 0 || L > (int64_t)a.cache.table_stride * ps))) {
+      bad = true;
+    } else if (hi > lo) {
+      const int64_t p0 = first / ps, p1 = (L - 1) / ps;
+      bad = bad_page(b, p0) | bad_page(b, p0 < p1 ? p0 + 1 : p0);
+      if (p0 + 1 < p1) long_s[atomicAdd(&n_long, 1)] = b;
+    }
+  }
+  __syncthreads();
+  for (int i = warp_id(); i < n_long; i += kThreads / 32) {
+    const int s = long_s[i];
+    const int64_t L = __ldg(a.seq_lens + s), first = L - (__ldg(a.cu + s + 1) - __ldg(a.cu + s));
+    for (int64_t p = first / ps + 2 + lane_id(); p <= (L - 1) / ps; p += 32) bad |= bad_page(s, p);
+  }
+  const bool any = __syncthreads_or(bad);
+  if (b == 0) *a.err = any ? kDevBadIndex : 0;
 }
 
 constexpr int kMaxTok = 16;
@@ -105,6 +142,10 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const Args a, con
   __shared__ int64_t off_s[kMaxTok], pos_s[kMaxTok];
   const int tid = threadIdx.x;
   const int64_t t0 = (int64_t)blockIdx.x * tok;
+  if (t0 >= a.T) {
+    check_batch(a);
+    return;
+  }
   for (int i = warp_id(); i < tok; i += kThreads / 32) {
     int64_t pos, off;
     locate(a, t0 + i, a.G * D, pos, off);
@@ -188,7 +229,12 @@ cudaError_t launch_d(const RopeAppendLaunch& p, const Args& a, cudaStream_t s) {
                                                                               : 5 * kThreads / 2;
   int tok = 1;
   while (tok < kMaxTok && 2 * tok * per_tok <= want) tok *= 2;
-  rope_append_kernel<D, IL><<<(unsigned)((p.T + tok - 1) / tok), kThreads, 0, s>>>(a, tok);
+  const unsigned ctas = (unsigned)((p.T + tok - 1) / tok) + (a.checked ? 1 : 0);
+  if (!a.checked) {
+    const cudaError_t e = cudaMemsetAsync(p.err, 0, sizeof(uint32_t), s);
+    if (e != cudaSuccess) return e;
+  }
+  rope_append_kernel<D, IL><<<ctas, kThreads, 0, s>>>(a, tok);
   return cudaGetLastError();
 }
 
@@ -213,6 +259,7 @@ cudaError_t launch_rope_append(const RopeAppendLaunch& p, cudaStream_t s) {
   a.T = p.T;
   a.q_out = static_cast<uint8_t*>(p.q_out);
   a.err = p.err;
+  a.checked = p.B <= kThreads;
   if (p.d == 128) return p.interleaved ? launch_d<128, true>(p, a, s) : launch_d<128, false>(p, a, s);
   return p.interleaved ? launch_d<64, true>(p, a, s) : launch_d<64, false>(p, a, s);
 }

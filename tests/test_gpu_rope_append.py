@@ -111,6 +111,47 @@ def test_many_sequences(msa):
     run(msa, 2, 1, 64, 64, False, 16, new, ctx)
 
 
+@pytest.mark.parametrize("B", [1, 31, 33, 256, 257, 600])
+def test_bad_entries_anywhere_in_a_batch(msa, B):
+    """One bad page id or length, in the first or last sequence, on a first, middle or last page:
+    recorded, whatever the number of sequences; a good batch clears the word again."""
+    H, G, d, page, cols = 2, 1, 64, 16, 8
+    cfg = msa.config(H, G, d, d)
+    new = [(5 * b) % 90 + 40 for b in range(B)]
+    cu = dc.offsets(new)
+    q, k, v = (dc.randn((cu[-1], n, d), i) for i, n in enumerate((H, G, G)))
+    lens = [n + (7 * b) % 30 for b, n in enumerate(new)]
+    lens = [min(n, page * cols) for n in lens]
+    new = [min(n, l) for n, l in zip(new, lens)]
+    table = np.arange(B * cols, dtype=np.int32).reshape(B, cols)
+    kc = torch.zeros((B * cols, page, G, d), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    ws = torch.full((256,), 0xFF, dtype=torch.uint8, device="cuda")
+
+    def call(tb, ls):
+        msa.msa_rope_append_paged(cfg, q, k, v, freqs(64),
+                                  msa.paged_kv(kc, vc, torch.from_numpy(tb).cuda()),
+                                  torch.tensor(cu).cuda(),
+                                  torch.tensor(ls, dtype=torch.int32).cuda(), workspace=ws)
+        return msa.msa_get_device_error(ws)
+    assert call(table, lens) == 0
+    for b in {0, B - 1}:
+        first, last = (lens[b] - new[b]) // page, (lens[b] - 1) // page
+        for p in {first, (first + last) // 2, last}:
+            tb = table.copy()
+            tb[b, p] = -1 if p == first else B * cols
+            assert call(tb, lens) == 0x201
+        for bad in (new[b] - 1, page * cols + 1):
+            ls = list(lens)
+            ls[b] = bad
+            assert call(table, ls) == 0x201
+        tb = table.copy()
+        tb[b, last + 1:] = -1  # not a page of the sequence
+        tb[b, :first] = -1
+        assert call(tb, lens) == 0
+    assert call(table, lens) == 0
+
+
 def test_bad_entries_are_recorded_and_skipped(msa):
     H, G, d, page = 2, 1, 64, 16
     cfg = msa.config(H, G, d, d)
