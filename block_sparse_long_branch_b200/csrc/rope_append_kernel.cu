@@ -80,9 +80,9 @@ __device__ __forceinline__ void locate(const Args& a, int64_t t, int row_elems, 
     L = __ldg(a.seq_lens + b);
   }
   const int64_t p = (int64_t)L - (end - t);
-  // offsets that are not ascending, a sequence with fewer keys than new tokens,
-  // or a row past the block table
-  if (t < begin || t >= end || p < t - begin ||
+  // offsets that are not ascending or pass T, a sequence with fewer keys than new
+  // tokens, or a row past the block table
+  if (begin < 0 || t < begin || t >= end || end > a.T || p < t - begin ||
       p >= (int64_t)a.cache.table_stride * a.cache.page_size) {
     if (lane == 0 && !a.checked) record_error(a.err, kDevBadIndex);
     return;

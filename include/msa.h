@@ -442,8 +442,8 @@ MSA_API msa_status_t msa_decode_static(const msa_config_t* cfg, const void* q, c
  * length with them, so row i is position seq_lens[b] - (cu_seqlens[b+1] - i).
  * Rows of the T given that lie behind cu_seqlens[B] are left as they are.  A
  * sequence whose seq_lens is smaller than its new tokens or beyond its row of
- * the block table is recorded as MSA_ERR_DEVICE_INDEX and skipped; offsets that
- * descend or pass T are recorded as well.
+ * the block table is recorded as MSA_ERR_DEVICE_INDEX and skipped, and so is one
+ * whose offsets descend or pass T.
  * Sequences must not share a page that one of them appends to.
  */
 typedef struct {

@@ -128,7 +128,7 @@ def test_bad_entries_anywhere_in_a_batch(msa, B):
     vc = torch.zeros_like(kc)
     ws = torch.full((256,), 0xFF, dtype=torch.uint8, device="cuda")
 
-    def call(tb, ls):
+    def call(tb, ls, cu=cu):
         msa.msa_rope_append_paged(cfg, q, k, v, freqs(64),
                                   msa.paged_kv(kc, vc, torch.from_numpy(tb).cuda()),
                                   torch.tensor(cu).cuda(),
@@ -145,6 +145,10 @@ def test_bad_entries_anywhere_in_a_batch(msa, B):
             ls = list(lens)
             ls[b] = bad
             assert call(table, ls) == 0x201
+        room = [page * cols] * B  # enough for any offsets
+        kc[(B - 1) * cols:], vc[(B - 1) * cols:] = 0, 0
+        assert call(table, room, cu[:-1] + [cu[-1] + 1]) == 0x201  # passes the tokens given
+        assert not kc[(B - 1) * cols:].any() and not vc[(B - 1) * cols:].any()
         tb = table.copy()
         tb[b, last + 1:] = -1  # not a page of the sequence
         tb[b, :first] = -1
