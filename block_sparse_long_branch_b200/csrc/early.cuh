@@ -30,8 +30,7 @@ cudaError_t launch_early(void (*kern)(Params...), int grid, int threads, int sme
 // it.  A kernel of its own, not a memset, because the kernel behind it may start
 // early: it finds all earlier work of the stream done, and waits for the zeros only
 // before it records an error, takes a ticket or ends (decode of one request of 4K:
-// 18.5 -> 16.4 us back to back).  It costs the host 2 us more than a memset does, so
-// calls that the host bounds have one (append of 16 tokens: 13.8 -> 15.8 us).
+// 18.5 -> 16.4 us back to back).  It costs the host 2 us more than a memset does.
 static __global__ void __launch_bounds__(256) clear_kernel(uint4* p, int64_t words) {
   pdl_launch_dependents();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
