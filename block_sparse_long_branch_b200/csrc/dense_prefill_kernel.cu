@@ -91,6 +91,10 @@ struct PrefillArgs {
   __nv_bfloat16* out;
   float* part_o;     // [slot][256][D]
   float2* part_ml;   // [slot][256] (log2-domain maximum, sum)
+  // Whether out and part_o are 32-byte aligned; callers promise 16.  Stores of 16 bytes
+  // throughout cost 6 % of a small prompt (one of 4K, 4 heads: 30.8 -> 32.6 us), 1 % of
+  // packed ones.
+  bool out32, part32;
   int32_t clear_err;
   uint32_t* err;
 };
@@ -1060,7 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (odd) add_odd(c, f);
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
-            st_global_32(dst + c + e, reinterpret_cast<const uint32_t*>(f + e));
+            st_global_32(dst + c + e, reinterpret_cast<const uint32_t*>(f + e), a.part32);
         }
         if (valid) a.part_ml[prow] = make_float2(m * a.scale_log2, l);
       } else if (cnt > 0) {
@@ -1078,8 +1082,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
-          st_global_32(dst + c, w);  // whole sectors: no staging for coalesced stores
-          st_global_32(dst + c + 16, w + 8);
+          st_global_32(dst + c, w, a.out32);  // whole sectors: no staging for coalesced stores
+          st_global_32(dst + c + 16, w + 8, a.out32);
         }
       }
       tc_fence_before();
@@ -1567,6 +1571,9 @@ cudaError_t launch_impl(const DensePrefillLaunch& p, cudaStream_t s, int* launch
   a.out = static_cast<__nv_bfloat16*>(p.out);
   a.part_o = p.part_o;
   a.part_ml = p.part_ml;
+  // every row of either is a multiple of 32 bytes behind its base
+  a.out32 = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
+  a.part32 = reinterpret_cast<uintptr_t>(p.part_o) % 32 == 0;
   a.clear_err = p.clear_err;
   a.err = p.err;
   // a warp per row of the split units, as far as there can be rows (those of

@@ -444,11 +444,17 @@ __device__ __forceinline__ float max3f_ordered(float a, float b, float c) {
   return d;
 }
 
-// 32 bytes to global memory in one store (32-byte aligned)
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
+// 32 bytes to global memory: in one store where p is 32-byte aligned (`aligned32`, the
+// same for the whole kernel), else in two of 16 bytes.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* w, bool aligned32) {
+  if (aligned32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
