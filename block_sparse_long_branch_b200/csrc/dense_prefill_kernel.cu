@@ -212,10 +212,12 @@ __device__ __forceinline__ void direct_seq(const DirectArgs& p, int b, uint32_t*
                                            int& n, int& pos) {
   lo = __ldg(p.cu + b);
   const int64_t hi = __ldg(p.cu + b + 1);
+  const int64_t first = __ldg(p.cu), last = __ldg(p.cu + p.B);
   const int L = __ldg(p.seq_lens + b);
   n = (int)(hi - lo);
   pos = L - n;
-  if (lo < 0 || hi < lo || hi > p.T || (n > 0 && (pos < 0 || L > p.table_rows))) {
+  if (lo < 0 || lo < first || hi < lo || hi > p.T || hi > last ||
+      (n > 0 && (pos < 0 || L > p.table_rows))) {
     record_error(err, kDevBadIndex);
     n = 0;
   }
@@ -1131,11 +1133,12 @@ __device__ __forceinline__ void plan_seq(const PlanArgs& p, const DenseOffsets& 
                                          int64_t& a, int& n, int& pos) {
   const int64_t lo = p.cu ? __ldg(p.cu + b) : off.cu[b];
   const int64_t hi = p.cu ? __ldg(p.cu + b + 1) : off.cu[b + 1];
+  const int64_t first = p.cu ? __ldg(p.cu) : 0, last = p.cu ? __ldg(p.cu + p.B) : p.T;
   const int L = p.seq_lens ? __ldg(p.seq_lens + b) : 0;
   a = lo;
   n = 0;
   pos = 0;
-  if (lo < 0 || hi < lo || hi > p.T) {
+  if (lo < 0 || lo < first || hi < lo || hi > p.T || hi > last) {
     record_error(p.err, kDevBadIndex);
     return;
   }

@@ -49,8 +49,18 @@ struct Args {
   int64_t T;
   uint8_t* q_out;
   uint32_t* err;
-  bool checked;  // the last CTA checks the batch (check_batch)
+  bool checked;  // the last CTA checks the batch (check_batch), else the last ones its offsets
+  int32_t checks;  // CTAs behind those of the tokens
 };
+
+// Whether a sequence of offsets [lo, hi) and length L takes part: the offsets ascend and
+// lie within those of the batch and the tokens given, and it has at least as many keys
+// as new tokens and no more than its row of the block table holds.
+__device__ __forceinline__ bool seq_ok(const Args& a, int64_t lo, int64_t hi, int64_t L,
+                                       int64_t first, int64_t last) {
+  return lo >= 0 && lo >= first && hi >= lo && hi <= last && hi <= a.T &&
+         (hi == lo || (L >= hi - lo && L <= (int64_t)a.cache.table_stride * a.cache.page_size));
+}
 
 // Where token t's row is: its position (-1: of no sequence, or of an invalid one)
 // and the element offset in the cache (-1: none).  A whole warp.
@@ -59,41 +69,63 @@ __device__ __forceinline__ void locate(const Args& a, int64_t t, int row_elems, 
   pos = off = -1;
   if (t >= a.T) return;
   const int lane = lane_id();
-  int b;
-  int64_t begin, end;
-  int L;
+  int b = -1;
+  int64_t end = 0;
+  int L = 0;
   if (a.B < 32) {  // all offsets and lengths in one round trip
     const int64_t c = lane <= a.B ? __ldg(a.cu + lane) : 0;
     const int l = lane < a.B ? __ldg(a.seq_lens + lane) : 0;
-    const unsigned m = __ballot_sync(0xffffffffu, lane < a.B && c <= t);
+    const int64_t c1 = __shfl_down_sync(0xffffffffu, c, 1);
+    const int64_t first = __shfl_sync(0xffffffffu, c, 0), last = __shfl_sync(0xffffffffu, c, a.B);
+    const unsigned m = __ballot_sync(
+        0xffffffffu, lane < a.B && c <= t && t < c1 && seq_ok(a, c, c1, l, first, last));
     if (m == 0) return;
     b = 31 - __clz(m);
-    begin = __shfl_sync(0xffffffffu, c, b);
-    end = __shfl_sync(0xffffffffu, c, b + 1);
+    end = __shfl_sync(0xffffffffu, c1, b);
     L = __shfl_sync(0xffffffffu, l, b);
-    if (t >= __shfl_sync(0xffffffffu, c, a.B)) return;
   } else {
-    if (t < __ldg(a.cu) || t >= __ldg(a.cu + a.B)) return;
-    b = find_seq(a.cu, a.B, t);
-    begin = __ldg(a.cu + b);
-    end = __ldg(a.cu + b + 1);
-    L = __ldg(a.seq_lens + b);
+    const int64_t first = __ldg(a.cu), last = __ldg(a.cu + a.B);
+    if (t < first || t >= last) return;
+    const int s = find_seq(a.cu, a.B, t);
+    const int64_t lo = __ldg(a.cu + s);
+    end = __ldg(a.cu + s + 1);
+    L = __ldg(a.seq_lens + s);
+    if (lo <= t && t < end && seq_ok(a, lo, end, L, first, last)) {
+      b = s;
+    } else {
+      // an invalid sequence; where offsets descend another may hold the token
+      for (int b0 = 0; b0 < a.B && b < 0; b0 += 32) {
+        const int i = b0 + lane;
+        const int64_t c = i < a.B ? __ldg(a.cu + i) : 0, c1 = i < a.B ? __ldg(a.cu + i + 1) : 0;
+        const int l = i < a.B ? __ldg(a.seq_lens + i) : 0;
+        const unsigned m =
+            __ballot_sync(0xffffffffu, c <= t && t < c1 && seq_ok(a, c, c1, l, first, last));
+        if (m == 0) continue;
+        const int k = __ffs(m) - 1;
+        b = b0 + k;
+        end = __shfl_sync(0xffffffffu, c1, k);
+        L = __shfl_sync(0xffffffffu, l, k);
+      }
+      if (b < 0) return;
+    }
   }
-  const int64_t p = (int64_t)L - (end - t);
-  // offsets that are not ascending or pass T, a sequence with fewer keys than new
-  // tokens, or a row past the block table
-  if (begin < 0 || t < begin || t >= end || end > a.T || p < t - begin ||
-      p >= (int64_t)a.cache.table_stride * a.cache.page_size) {
-    if (lane == 0 && !a.checked) record_error(a.err, kDevBadIndex);
-    return;
-  }
-  pos = p;
-  const int pg = __ldg(a.cache.block_table + (int64_t)b * a.cache.table_stride + p / a.cache.page_size);
+  pos = (int64_t)L - (end - t);
+  const int pg =
+      __ldg(a.cache.block_table + (int64_t)b * a.cache.table_stride + pos / a.cache.page_size);
   if (pg < 0 || pg >= a.cache.num_pages) {
     if (lane == 0 && !a.checked) record_error(a.err, kDevBadIndex);
     return;
   }
-  off = (int64_t)pg * a.cache.page_stride + (p % a.cache.page_size) * (int64_t)row_elems;
+  off = (int64_t)pg * a.cache.page_stride + (pos % a.cache.page_size) * (int64_t)row_elems;
+}
+
+// The offsets and lengths of 256 sequences of a larger batch, a thread each; bad page ids
+// are recorded by the CTAs that meet them.
+__device__ __forceinline__ void check_offsets(const Args& a, int64_t b) {
+  if (b >= a.B) return;
+  if (!seq_ok(a, __ldg(a.cu + b), __ldg(a.cu + b + 1), __ldg(a.seq_lens + b), __ldg(a.cu),
+              __ldg(a.cu + a.B)))
+    record_error(a.err, kDevBadIndex);
 }
 
 // The error word of a batch of up to kThreads sequences, written whole by one CTA that
@@ -113,8 +145,7 @@ __device__ __forceinline__ void check_batch(const Args& a) {
   if (b < a.B) {
     const int64_t lo = __ldg(a.cu + b), hi = __ldg(a.cu + b + 1);
     const int64_t L = __ldg(a.seq_lens + b), first = L - (hi - lo);
-    if (lo < 0 || hi < lo || hi > a.T ||
-        (hi > lo && (first < 0 || L > (int64_t)a.cache.table_stride * ps))) {
+    if (!seq_ok(a, lo, hi, L, __ldg(a.cu), __ldg(a.cu + a.B))) {
       bad = true;
     } else if (hi > lo) {
       const int64_t p0 = first / ps, p1 = (L - 1) / ps;
@@ -143,7 +174,10 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const Args a, con
   const int tid = threadIdx.x;
   const int64_t t0 = (int64_t)blockIdx.x * tok;
   if (t0 >= a.T) {
-    check_batch(a);
+    if (a.checked)
+      check_batch(a);
+    else
+      check_offsets(a, (int64_t)(blockIdx.x - (gridDim.x - a.checks)) * kThreads + tid);
     return;
   }
   for (int i = warp_id(); i < tok; i += kThreads / 32) {
@@ -229,7 +263,7 @@ cudaError_t launch_d(const RopeAppendLaunch& p, const Args& a, cudaStream_t s) {
                                                                               : 5 * kThreads / 2;
   int tok = 1;
   while (tok < kMaxTok && 2 * tok * per_tok <= want) tok *= 2;
-  const unsigned ctas = (unsigned)((p.T + tok - 1) / tok) + (a.checked ? 1 : 0);
+  const unsigned ctas = (unsigned)((p.T + tok - 1) / tok) + a.checks;
   if (!a.checked) {
     const cudaError_t e = cudaMemsetAsync(p.err, 0, sizeof(uint32_t), s);
     if (e != cudaSuccess) return e;
@@ -260,6 +294,7 @@ cudaError_t launch_rope_append(const RopeAppendLaunch& p, cudaStream_t s) {
   a.q_out = static_cast<uint8_t*>(p.q_out);
   a.err = p.err;
   a.checked = p.B <= kThreads;
+  a.checks = (p.B + kThreads - 1) / kThreads;
   if (p.d == 128) return p.interleaved ? launch_d<128, true>(p, a, s) : launch_d<128, false>(p, a, s);
   return p.interleaved ? launch_d<64, true>(p, a, s) : launch_d<64, false>(p, a, s);
 }

@@ -440,10 +440,12 @@ MSA_API msa_status_t msa_decode_static(const msa_config_t* cfg, const void* q, c
  * int32 [B]) describe a step to the append and to the attention: sequence b's
  * new tokens are rows cu_seqlens[b] .. cu_seqlens[b+1]-1, and seq_lens[b] is its
  * length with them, so row i is position seq_lens[b] - (cu_seqlens[b+1] - i).
- * Rows of the T given that lie behind cu_seqlens[B] are left as they are.  A
- * sequence whose seq_lens is smaller than its new tokens or beyond its row of
- * the block table is recorded as MSA_ERR_DEVICE_INDEX and skipped, and so is one
- * whose offsets descend or pass T.
+ * Rows of the T given that lie before cu_seqlens[0] or behind cu_seqlens[B] are
+ * left as they are.  A sequence whose seq_lens is smaller than its new tokens or
+ * beyond its row of the block table is recorded as MSA_ERR_DEVICE_INDEX and
+ * skipped, and so is one whose offsets descend, pass T or leave cu_seqlens[0] ..
+ * cu_seqlens[B].  Where a descent gives a row to two valid sequences, what the
+ * valid sequences' rows then hold is not defined.
  * Sequences must not share a page that one of them appends to.
  */
 typedef struct {
