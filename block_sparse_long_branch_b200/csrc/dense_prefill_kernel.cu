@@ -43,6 +43,7 @@
 
 #include "early.cuh"
 #include "kernels.h"
+#include "ring.h"
 #include "sm100.cuh"
 #include "tmap.h"
 
@@ -599,8 +600,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t* ring = is_v ? sV : sK;
       uint32_t slot = 0, phase = 0;       // of the next tile
       uint32_t regular = 0, special = 0;  // V tiles of both kinds so far
-      uint64_t* last_full = nullptr;     // of the last copy
-      uint32_t last_par = 0;
       uint32_t qn[2] = {0, 0};      // Q tiles loaded so far
       bool ok = true;
       const int box_rows = a.box_rows, boxes = kKeys / box_rows;  // a lane per box of a tile
@@ -648,24 +647,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j == 0) load_q(u, 0);
           if (!ok) break;
           uint64_t* full;
-          uint32_t par;
-          if (!is_v) {
+          if (!is_v)
             full = &bar_k_full[slot];
-            par = phase;
-          } else if (j < part0) {
-            full = &bar_v_full[regular % VS];
-            par = (regular++ / VS) & 1;
-          } else {
-            full = &bar_spec[special % VS];
-            par = (special++ / VS) & 1;
-          }
+          else if (j < part0)
+            full = &bar_v_full[regular++ % VS];
+          else
+            full = &bar_spec[special++ % VS];
           ok = __all_sync(0xffffffffu,
                           mbar_wait(&empty[slot], phase ^ 1, abort_flag, a.err, kDevTimeoutMma));
-          if (!ok) break;
+          if (!ok) {
+            if (is_v) --(j < part0 ? regular : special);  // not issued
+            break;
+          }
           if (elect_one()) mbar_arrive_expect_tx(full, (uint32_t)(nbox * box_rows * D * 2));
           __syncwarp();
-          last_full = full;
-          last_par = par;
           // One copy after the other with operands known to be the same in the
           // whole warp; a lane each, they are issued in a loop over the lanes.
           uint8_t* dst = ring + slot * Cfg::kTileBytes;
@@ -684,15 +679,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (lane == 0 && *abort_flag) {
-        // the copies in flight must land before the CTA's shared memory goes
+        // The copies in flight must land before the CTA's shared memory goes.  (Where
+        // the flag comes up after this, a wait of 2 s has run out behind them.)
         volatile int no_abort = 0;
         for (int i = 0; i < 2; ++i)
           if (qn[i]) mbar_wait(&bar_q_full[i], (qn[i] - 1) & 1, &no_abort, nullptr, 0);
-        if (last_full) mbar_wait(last_full, last_par, &no_abort, nullptr, 0);
+#pragma unroll 1
         for (uint32_t i = 0; i < slots; ++i) {
-          // whichever copies are behind the last one: a microsecond or two
-          const uint64_t t0 = global_timer_ns();
-          while (global_timer_ns() - t0 < 20000) {
+          if (is_v) {
+            // the i-th from the end of both kinds, see ring_parity
+            const uint32_t r = regular + VS - 1 - i, s = special + VS - 1 - i;
+            if (r >= VS) mbar_wait(&bar_v_full[r % VS], ring_parity(r, VS), &no_abort, nullptr, 0);
+            if (s >= VS) mbar_wait(&bar_spec[s % VS], ring_parity(s, VS), &no_abort, nullptr, 0);
+          } else {
+            mbar_wait(&bar_k_full[i], ring_last_parity(i, slot, phase), &no_abort, nullptr, 0);
           }
         }
       }
