@@ -38,8 +38,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // ROWS: head rows of an item (8 or 16)
 template <int D, int ROWS>
 struct DecodeCfg {
-  // keys per step: 8 KiB of K and V either way.  At d = 64 steps of 16 keys left a
-  // warp waiting on its own chain of instructions (decode_ragged: see below)
+  // keys per step: 8 KiB of K and V either way.  At d = 64 steps of 16 keys leave a
+  // warp waiting on its own chain of instructions (52 requests of 1 to 16K tokens, 32
+  // heads in 8 groups: 98 us, with steps of 32 keys 77)
   static constexpr int kStep = D == 128 ? 16 : 32;
   static constexpr int kHalf = kStep * D * 2;  // K or V of one step
   static constexpr int kStageBytes = 2 * kHalf;
@@ -187,8 +188,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- groups at a time, and the line ----
   // gw: as many groups as divide the items evenly, while a share keeps 16 steps
   // and a bundle spans 16 shares at most on average: its parts are joined by one
-  // CTA (one sequence of 1M, 8 groups: 745 us with all eight at a time, 660 with
-  // one; 16 of 256K and one of 1M: 3.07 ms with eight, 3.33 with two).
+  // CTA (8 groups, all eight at a time or fewer: one sequence of 1M 749 -> 644 us, of
+  // 30K 86 -> 35).  Where both are met it decides little: 16 of 256K and one of 1M take
+  // 3.06 to 3.35 ms with eight, from one GPU to another, and 3.14 to 3.17 with one to four.
   int gw = (items & 7) == 0 ? 8 : (items & 3) == 0 ? 4 : (items & 1) == 0 ? 2 : 1;
   while (gw > 1 && (total * items < 16ll * gw * gridDim.x || seqs * items * 16 < (long long)gw * gridDim.x))
     gw >>= 1;

@@ -79,7 +79,7 @@ struct PrefillCfg {
 
 struct PrefillArgs {
   int32_t H, G, HG, TT;
-  float scale, scale_log2;
+  float scale_log2;
   const DenseUnit* units;  // device plan: the units (each for all groups) and their number
   const int32_t* n_units;
   int32_t* next_unit;      // units taken beyond the first of every CTA
@@ -101,7 +101,7 @@ struct PrefillArgs {
 };
 
 // The units of a small batch whose lengths the host knows travel as a kernel
-// parameter: no planning kernel in front (prefill of 128 tokens: 14.4 -> 8.5 us).
+// parameter: no planning kernel in front (prefill of 128 tokens, replayed: 13.0 -> 9.3 us).
 constexpr int kHostUnits = 128;
 enum PlanMode { kPlanned, kHost, kDirect };
 struct HostUnits {
@@ -206,7 +206,7 @@ __host__ __device__ __forceinline__ int part_begin(int k, int parts, int len, in
 
 constexpr int kPartCost = 3;  // a unit's or a part's cost beside its key tiles, in key tiles
 constexpr int kJoinCost = 7;  // partial results stored, read and joined, likewise: units of 27
-                              // key tiles split to take 26 lost 8 of 78 us
+                              // key tiles split to take 26 took 86 us instead of 66
 
 // new tokens [lo, lo+n) of sequence b, the first at position pos; n = 0: none, or invalid
 __device__ __forceinline__ void direct_seq(const DirectArgs& p, int b, uint32_t* err, int64_t& lo,
@@ -236,9 +236,11 @@ __device__ __forceinline__ int direct_tiles(int n, int pos, int off, int TT, int
 //  * the units of all groups as one line, cut into equal shares, one a CTA, which
 //    leaves no CTA idle (100 units of one length do not make 148 parts): where that
 //    shortens the longest CTA's work by an eighth.  It costs the units of a group
-//    their common pace through the keys, which then come from memory several times:
-//    52 units over 30K keys (32 heads in 4 groups) 248 -> 220 us, 109 over 0.1K to
-//    50K (16 heads in one) 201 -> 131, but 512 units over 1K to 30K 735 -> 956.
+//    their common pace through the keys, which then come from memory several times.
+//    Parts -> line, whole calls: 112 units over 0.1K to 50K (16 heads in one group)
+//    353 -> 220 us, 52 over 30K (32 heads in 4) 238 -> 222, 88 (64 in 8) 426 -> 397;
+//    104 (64 in 8) lose a little, 454 -> 471, and over 10K keys 164 -> 175.  More
+//    units than CTAs lost about a third, their keys read eleven times from memory.
 struct PlanUnit {
   int seq, off;  // sequence, first of its new tokens
   int nt, w;     // key tiles, weight
@@ -539,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The warp's r-th unit; false after the last.  A CTA starts with its own number
   // and takes the next one of the line whenever it has loaded a unit: longest
   // first, so the CTAs end nearly together whatever the lengths (chunks of four
-  // caches of 1K to 30K: 917 -> 830 us against a fixed order).
+  // caches of 1K to 30K: 943 -> 866 us against a fixed order).
   // With kDirect warp 8 hands out the CTA's own unit, or the parts of its share.
   auto next_unit = [&](int r, Unit& u) {
     constexpr bool kOwn = MODE == kDirect;
@@ -1559,7 +1561,6 @@ cudaError_t launch_impl(const DensePrefillLaunch& p, cudaStream_t s, int* launch
   a.G = p.G;
   a.HG = HG;
   a.TT = TT;
-  a.scale = p.scale;
   a.scale_log2 = p.scale * kLog2e;
   a.units = p.units;
   a.n_units = p.counts;

@@ -12,7 +12,8 @@
 // Memory bound: every element is read and written once.  A CTA takes a few tokens:
 // their rows in the cache and their sines and cosines first, then 16 dimensions of
 // a head per thread and turn (two 16-byte pieces that hold 8 whole pairs in either
-// layout).  A 32K prompt of 64 + 2 x 8 heads of 128 moves at 5.8 to 6.2 TB/s.
+// layout).  A 32K prompt of 64 + 2 x 8 heads of 128 takes 218 to 234 us from one GPU to
+// another: 5.7 to 6.2 TB/s.
 #include "kernels.h"
 #include "sm100.cuh"
 
@@ -130,8 +131,8 @@ __device__ __forceinline__ void check_offsets(const Args& a, int64_t b) {
 
 // The error word of a batch of up to kThreads sequences, written whole by one CTA that
 // looks at every length and page id while the others work: no memset in front of the
-// kernel (16 tokens: 13.6 -> 12.7 us, the rest of it the host's).  A thread per sequence; pages beyond a sequence's
-// second by the warps.
+// kernel (16 tokens, issued one by one: 14.8 -> 12.8 us; 4.3 of it the kernel's).  A
+// thread per sequence; pages beyond a sequence's second by the warps.
 __device__ __forceinline__ void check_batch(const Args& a) {
   __shared__ int long_s[kThreads], n_long;
   const int b = threadIdx.x, ps = a.cache.page_size;
